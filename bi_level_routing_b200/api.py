@@ -8,8 +8,10 @@ CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import re
+from typing import NamedTuple
 
 import torch
 
@@ -19,6 +21,8 @@ HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))
 STATUS = {0: "BRA_OK", 1: "BRA_ERR_INVALID_ARG", 2: "BRA_ERR_UNSUPPORTED", 3: "BRA_ERR_CUDA",
           4: "BRA_ERR_INDEX", 5: "BRA_ERR_TIMEOUT"}
 DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+NORM_KINDS = {"layer": 0, "rms": 1}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ATTEND_KERNELS = {"auto": 0, "simt": 1, "gather_mma": 2, "dense_mma": 3, "gather_umma": 4, "region_mma": 5}
 
 _lib = None
@@ -52,6 +56,14 @@ def lib() -> ctypes.CDLL:
     L.bra_lepe.argtypes = [vp, vp, vp, vp, I, I, I, I, I, vp]
     L.bra_forward_lepe.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, I, I, I, I, I, I, I, I, vp]
     L.bra_attend_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, I, I, I, I, I, I, I, I, vp]
+    F, I64 = ctypes.c_float, ctypes.c_int64
+    L.bra_diff_attend.argtypes = [vp, vp, vp, vp, vp, vp, I, I, I, I, I, I, I, I, vp]
+    L.bra_forward_diff.argtypes = [vp, vp, vp, vp, vp, vp, I, I, I, I, I, I, I, I, vp]
+    L.bra_diff_attend_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, I, I, I, I, I, I, I, I, vp]
+    L.bra_rope.argtypes = [vp, vp, vp, vp, vp, vp, I64, I64, I, I, I, I, I, I, I, I, I, F, I, vp]
+    L.bra_norm_residual.argtypes = [vp, vp, vp, I, vp, vp, vp, vp, F, F, I, vp, vp, I, I, I, I, I, vp]
+    L.bra_norm_residual_backward.argtypes = [vp, vp, vp, vp, vp, I, vp, vp, vp, vp, F, F, I, vp, vp, vp, vp, vp, vp, vp,
+                                             I, I, I, I, I, vp]
     L.bra_selftest_wait_timeout.argtypes = [ctypes.c_uint, vp]
     L.bra_set_attend_kernel.argtypes = [I]
     L.bra_set_max_ctas.argtypes = [I]
@@ -65,7 +77,9 @@ def lib() -> ctypes.CDLL:
     L.bra_last_error_message.restype = ctypes.c_char_p
     for name in ("bra_route", "bra_attend", "bra_forward", "bra_forward_host", "bra_set_attend_kernel", "bra_set_max_ctas",
                  "bra_route_heads", "bra_attend_heads", "bra_forward_heads", "bra_forward_auto_pad", "bra_lepe",
-                 "bra_forward_lepe", "bra_attend_backward", "bra_selftest_wait_timeout",
+                 "bra_forward_lepe", "bra_attend_backward", "bra_selftest_wait_timeout", "bra_diff_attend",
+                 "bra_forward_diff", "bra_diff_attend_backward", "bra_rope", "bra_norm_residual",
+                 "bra_norm_residual_backward",
                  "bra_selected_attend_kernel", "bra_check_device_error", "bra_kernels_per_call"):
         getattr(L, name).restype = I
     _lib = L
@@ -297,6 +311,227 @@ def attend_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, idx: torc
                                      dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, W, C, heads, n_win,
                                      idx.shape[-1], DTYPES[q.dtype], _stream(q.device)), "bra_attend_backward")
     return dq, dk, dv
+
+
+def _on_device(device, fn, *args) -> int:
+    """fn(*args, stream) with `device` current and its current stream: the tensors' device need not be
+    the caller's."""
+    if torch.cuda.current_device() == device.index:
+        return fn(*args, _stream(device))
+    with torch.cuda.device(device):
+        return fn(*args, _stream(device))
+
+
+def _routed(idx: torch.Tensor, q: torch.Tensor, n_win: int):
+    if (idx.dim() != 3 or idx.shape[:2] != (q.shape[0], n_win * n_win) or idx.dtype != torch.int32
+            or not idx.is_contiguous() or idx.device != q.device):
+        raise ValueError("idx must be a contiguous int32 [B, n_win^2, topk] tensor on q's device")
+
+
+def _vector(t: torch.Tensor | None, name: str, shapes, device):
+    """A contiguous fp32 tensor of one of `shapes` on `device`, or None."""
+    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) not in shapes or not t.is_contiguous()
+                          or t.device != device):
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {' or '.join(map(str, shapes))} on "
+                         f"{device}")
+    return t
+
+
+def _ptr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _output(t: torch.Tensor | None, like: torch.Tensor, name: str) -> torch.Tensor:
+    if t is None:
+        return torch.empty_like(like)
+    _same(like, (name, t))
+    return t
+
+
+def diff_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, idx: torch.Tensor, lam: torch.Tensor, heads: int,
+                n_win: int, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Differential attention over the routed regions: per head the map of the first half of its q and k
+    channels minus lam[head] times the map of the second half, times v. lam: float32 [heads]."""
+    B, H, W, C = _shape(q, "q")
+    _same(q, ("k", k), ("v", v))
+    _routed(idx, q, n_win)
+    _vector(lam, "lam", [(heads,)], q.device)
+    out = _output(out, q, "out")
+    _check(_on_device(q.device, lib().bra_diff_attend, q.data_ptr(), k.data_ptr(), v.data_ptr(), idx.data_ptr(),
+                      lam.data_ptr(), out.data_ptr(), B, H, W, C, heads, n_win, idx.shape[-1], DTYPES[q.dtype]),
+           "bra_diff_attend")
+    return out
+
+
+def forward_diff(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor, n_win: int, topk: int, heads: int,
+                 out: torch.Tensor | None = None, idx: torch.Tensor | None = None):
+    """Routing, then differential attention. Returns (out, idx)."""
+    B, H, W, C = _shape(q, "q")
+    _same(q, ("k", k), ("v", v))
+    _vector(lam, "lam", [(heads,)], q.device)
+    out = _output(out, q, "out")
+    if idx is None:
+        idx = torch.empty((B, n_win * n_win, topk), dtype=torch.int32, device=q.device)
+    _routed(idx, q, n_win)
+    if idx.shape[-1] != topk:
+        raise ValueError("idx must be a contiguous int32 [B, n_win^2, topk] tensor")
+    _check(_on_device(q.device, lib().bra_forward_diff, q.data_ptr(), k.data_ptr(), v.data_ptr(), idx.data_ptr(),
+                      lam.data_ptr(), out.data_ptr(), B, H, W, C, heads, n_win, topk, DTYPES[q.dtype]),
+           "bra_forward_diff")
+    return out, idx
+
+
+def diff_attend_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, idx: torch.Tensor, lam: torch.Tensor,
+                         dout: torch.Tensor, heads: int, n_win: int, dq: torch.Tensor | None = None,
+                         dk: torch.Tensor | None = None, dv: torch.Tensor | None = None,
+                         dlam: torch.Tensor | None = None):
+    """(dq, dk, dv, dlam): gradients of sum(dout * diff_attend(q, k, v, idx, lam)), idx fixed. dq, dk and dv
+    have q's type, dlam is float32 [heads]; the same bits on every run."""
+    B, H, W, C = _shape(q, "q")
+    _same(q, ("k", k), ("v", v), ("dout", dout))
+    _routed(idx, q, n_win)
+    _vector(lam, "lam", [(heads,)], q.device)
+    dq, dk, dv = _output(dq, q, "dq"), _output(dk, q, "dk"), _output(dv, q, "dv")
+    dlam = torch.empty_like(lam) if dlam is None else _vector(dlam, "dlam", [(heads,)], q.device)
+    _check(_on_device(q.device, lib().bra_diff_attend_backward, q.data_ptr(), k.data_ptr(), v.data_ptr(), idx.data_ptr(),
+                      lam.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dlam.data_ptr(), B, H,
+                      W, C, heads, n_win, idx.shape[-1], DTYPES[q.dtype]), "bra_diff_attend_backward")
+    return dq, dk, dv, dlam
+
+
+def rope(q: torch.Tensor, k: torch.Tensor | None, freqs: torch.Tensor, heads: int, layout: str = "half", axes: int = 2,
+         origin: tuple[int, int] = (0, 0), pos: torch.Tensor | None = None, mscale: float = 1.0, inverse: bool = False,
+         q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None):
+    """Rotary positions of q and k (k may be None). The first 2 * axes * len(freqs) channels of each head are
+    turned: pairs (i, i + n) of each axis' block ("half") or (2i, 2i + 1) ("interleaved") by position * freqs[i].
+    Positions: the token's row and column (axes=2) or raster number (axes=1) from `origin`, or pos, int32
+    [B, H, W, axes]. inverse=True takes gradients back. q_out may be q, k_out k (in place).
+    Returns (q_out, k_out). See rope_frequencies for freqs and mscale."""
+    B, H, W, C = _shape(q, "q")
+    if k is not None:
+        _same(q, ("k", k))
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _vector(freqs, "freqs", [(freqs.numel(),)], q.device)
+    if pos is not None and (tuple(pos.shape) != (B, H, W, axes) or pos.dtype != torch.int32 or not pos.is_contiguous()
+                            or pos.device != q.device):
+        raise ValueError("pos must be a contiguous int32 [B, H, W, axes] tensor on q's device")
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
+    q_out = _output(q_out, q, "q_out")
+    if k is not None:
+        k_out = _output(k_out, k, "k_out")
+    _check(_on_device(q.device, lib().bra_rope, q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), freqs.data_ptr(),
+                      _ptr(pos), int(origin[0]), int(origin[1]), B, H, W, C, heads, freqs.numel(), axes,
+                      ROPE_LAYOUTS[layout], int(inverse), float(mscale), DTYPES[q.dtype]), "bra_rope")
+    return q_out, k_out
+
+
+def rope_frequencies(n: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     trained_extent: int | None = None, device=None) -> tuple[torch.Tensor, float]:
+    """(freqs float32 [n], mscale) for `rope`: freqs[i] = base^(-i / n), stretched by `factor` for maps or
+    sequences that much longer than the trained ones:
+      "linear"  every frequency divided by factor (positions interpolated);
+      "ntk"     base multiplied by factor^(n / (n - 1)): the fastest stays, the slowest is divided by factor;
+      "yarn"    frequencies that turn more than 32 times over trained_extent positions stay, those that turn
+                less than once are divided by factor, a linear ramp (in the number of the pair) between;
+                mscale = 0.1 ln(factor) + 1."""
+    if n <= 0 or not base > 1.0 or not factor >= 1.0:
+        raise ValueError("n must be positive, base above 1 and factor at least 1")
+    i = torch.arange(n, dtype=torch.float64)
+    mscale = 1.0
+    if scaling == "ntk" and n > 1:
+        base = base * factor ** (n / (n - 1))
+    freqs = base ** (-i / n)
+    if scaling == "linear" or (scaling == "ntk" and n == 1):
+        freqs = freqs / factor
+    elif scaling == "yarn":
+        if not trained_extent or trained_extent <= 0:
+            raise ValueError("yarn scaling needs trained_extent, the positions seen in training")
+        # the (real) pair numbers that turn 32 times and once over the trained extent
+        fast, slow = (n * math.log(trained_extent / (turns * 2 * math.pi)) / math.log(base) for turns in (32, 1))
+        low, high = max(math.floor(fast), 0), min(math.ceil(slow), n - 1)
+        ramp = ((i - low) / max(high - low, 1e-3)).clamp(0, 1)
+        freqs = freqs * (1 - ramp) + freqs / factor * ramp
+        mscale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in ("none", "ntk"):
+        raise ValueError(f"scaling must be none, linear, ntk or yarn, got {scaling!r}")
+    return freqs.float().to(device), mscale
+
+
+def _norm_arguments(x, h, gate, post_weight, post_bias, pre_weight, pre_bias, alpha, eps, kind):
+    """Checks the arguments both norm calls share; returns (shape, gate_images, kind code)."""
+    B, H, W, C = _shape(x, "x")
+    if h is not None:
+        _same(x, ("h", h))
+    for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("pre_weight", pre_weight),
+                    ("pre_bias", pre_bias)):
+        _vector(t, name, [(C,)], x.device)
+    _vector(gate, "gate", [(C,), (B, C)], x.device)
+    if kind not in NORM_KINDS:
+        raise ValueError(f"kind must be one of {sorted(NORM_KINDS)}, got {kind!r}")
+    return (B, H, W, C), (0 if gate is None else 1 if gate.dim() == 1 else B), NORM_KINDS[kind]
+
+
+def norm_residual(x: torch.Tensor, h: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                  post_weight: torch.Tensor | None = None, post_bias: torch.Tensor | None = None,
+                  pre_weight: torch.Tensor | None = None, pre_bias: torch.Tensor | None = None, alpha: float = 1.0,
+                  eps: float = 1e-6, kind: str = "layer", s_out: torch.Tensor | None = None,
+                  y_out: torch.Tensor | None = None):
+    """The norms around a block in one pass: s = alpha * x + gate * (norm(h) * post_weight + post_bias) and
+    y = norm(s) * pre_weight + pre_bias, norm a LayerNorm or an RMS norm (kind "layer", "rms"). Without
+    post_weight h is taken as it is, without h s = alpha * x, without pre_weight there is no y. Weights, biases:
+    float32 [C]; gate: float32 [C] or, one for each image, [B, C]. Returns (s, y); s is None where h is None
+    (unless s_out is given), y where pre_weight is None."""
+    shape, gates, code = _norm_arguments(x, h, gate, post_weight, post_bias, pre_weight, pre_bias, alpha, eps, kind)
+    if h is not None or s_out is not None:
+        s_out = _output(s_out, x, "s_out")
+    if pre_weight is not None:
+        y_out = _output(y_out, x, "y_out")
+    elif y_out is not None:
+        raise ValueError("y_out without pre_weight")
+    _check(_on_device(x.device, lib().bra_norm_residual, x.data_ptr(), _ptr(h), _ptr(gate), gates, _ptr(post_weight),
+                      _ptr(post_bias), _ptr(pre_weight), _ptr(pre_bias), float(alpha), float(eps), code, _ptr(s_out),
+                      _ptr(y_out), *shape, DTYPES[x.dtype]), "bra_norm_residual")
+    return s_out, y_out
+
+
+class NormGrads(NamedTuple):
+    """Gradients of norm_residual by its inputs, None for inputs that were not given."""
+    dx: torch.Tensor
+    dh: torch.Tensor | None
+    dgate: torch.Tensor | None
+    dpost_weight: torch.Tensor | None
+    dpost_bias: torch.Tensor | None
+    dpre_weight: torch.Tensor | None
+    dpre_bias: torch.Tensor | None
+
+
+def norm_residual_backward(x: torch.Tensor, h: torch.Tensor | None, dy: torch.Tensor | None, ds: torch.Tensor | None,
+                           gate: torch.Tensor | None = None, post_weight: torch.Tensor | None = None,
+                           post_bias: torch.Tensor | None = None, pre_weight: torch.Tensor | None = None,
+                           pre_bias: torch.Tensor | None = None, alpha: float = 1.0, eps: float = 1e-6,
+                           kind: str = "layer", dx: torch.Tensor | None = None,
+                           dh: torch.Tensor | None = None) -> NormGrads:
+    """Gradients of sum(ds * s) + sum(dy * y) of norm_residual with the same arguments. dy is given exactly where
+    pre_weight is; ds may be None (no gradient of s). dx and dh have x's type, the others are float32 of their
+    inputs' shapes; the same bits on every run."""
+    shape, gates, code = _norm_arguments(x, h, gate, post_weight, post_bias, pre_weight, pre_bias, alpha, eps, kind)
+    for name, t in (("dy", dy), ("ds", ds)):
+        if t is not None:
+            _same(x, (name, t))
+    dx = _output(dx, x, "dx")
+    if h is not None:
+        dh = _output(dh, x, "dh")
+    elif dh is not None:
+        raise ValueError("dh without h")
+    dgate, dpw, dpb, dnw, dnb = (None if t is None else torch.empty_like(t)
+                                 for t in (gate, post_weight, post_bias, pre_weight, pre_bias))
+    _check(_on_device(x.device, lib().bra_norm_residual_backward, x.data_ptr(), _ptr(h), _ptr(dy), _ptr(ds), _ptr(gate),
+                      gates, _ptr(post_weight), _ptr(post_bias), _ptr(pre_weight), _ptr(pre_bias), float(alpha), float(eps),
+                      code, dx.data_ptr(), _ptr(dh), _ptr(dgate), _ptr(dpw), _ptr(dpb), _ptr(dnw), _ptr(dnb), *shape,
+                      DTYPES[x.dtype]), "bra_norm_residual_backward")
+    return NormGrads(dx, dh, dgate, dpw, dpb, dnw, dnb)
 
 
 def check_device_error(device=None) -> int:

@@ -10,6 +10,7 @@
 #include <string>
 
 #include "bra.h"
+#include "bra_diff.cuh"
 #include "bra_launch.h"
 
 namespace {
@@ -92,8 +93,9 @@ bra_status device_state(DeviceState **out)
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Shape checks shared by every entry point (pointers are checked by the callers).
+// routes: the call takes region means (its rows of a region must fit their kernel).
 bra_status check_shape(int B, int H, int W, int C, int heads, int n_win, int topk, bra_dtype dtype,
-                       bra::Geometry *g)
+                       bra::Geometry *g, bool routes = true)
 {
     if (dtype != BRA_F32 && dtype != BRA_BF16) return BRA_ERR_INVALID_ARG;
     if (B < 0 || H <= 0 || W <= 0 || C <= 0 || heads <= 0 || n_win <= 0 || topk <= 0) return BRA_ERR_INVALID_ARG;
@@ -118,7 +120,7 @@ bra_status check_shape(int B, int H, int W, int C, int heads, int n_win, int top
     g->hd = C / heads;
     g->N = H * W;
     // The means kernel holds one region's row segment (wr tokens x C channels) in shared memory.
-    if ((long long)g->wr * C * elem > 16LL * bra::kMaxMeansVectors) return BRA_ERR_UNSUPPORTED;
+    if (routes && (long long)g->wr * C * elem > 16LL * bra::kMaxMeansVectors) return BRA_ERR_UNSUPPORTED;
     return BRA_OK;
 }
 
@@ -682,6 +684,307 @@ bra_status bra_attend_backward(const void *q, const void *k, const void *v, cons
     const cudaError_t e = bra::launch_attend_backward(q, k, v, idx, dout, dq, dk, dv, g, dtype == BRA_BF16,
                                                       st->error_word, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? BRA_OK : cuda_fail(e, "backward kernel");
+}
+
+// ---------------------------------------------------------------- differential attention
+
+// The sizes both passes take: heads of a multiple of 8 channels, at most 128.
+static bra_status check_diff(int B, int H, int W, int C, int heads, int n_win, int topk, bra_dtype dtype, bool routes,
+                             bra::Geometry *g)
+{
+    const bra_status s = check_shape(B, H, W, C, heads, n_win, topk, dtype, g, routes);
+    if (s != BRA_OK) return s;
+    if (g->hd % 8 != 0 || g->hd > 128) return BRA_ERR_UNSUPPORTED;
+    return BRA_OK;
+}
+
+static bra_status diff_attend_impl(const void *q, const void *k, const void *v, const int32_t *idx, const float *lambda,
+                                   void *out, const bra::Geometry &g, bra_dtype dtype, cudaStream_t stream)
+{
+    DeviceState *st = nullptr;
+    const bra_status s = device_state(&st);
+    if (s != BRA_OK) return s;
+    bra::DiffArgs a = {};
+    bra::diff_plan(a, g);
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.idx = idx;
+    a.lam = lambda;
+    a.out = out;
+    a.err = st->error_word;
+    const bool bf16 = dtype == BRA_BF16;
+    const cudaError_t e = bf16 && bra::diff_mma_supports(g) ? bra::launch_diff_attend_mma(a, stream)
+                                                            : bra::launch_diff_simt(a, false, bf16, stream);
+    return e == cudaSuccess ? BRA_OK : cuda_fail(e, "differential attention kernel");
+}
+
+bra_status bra_diff_attend(const void *q, const void *k, const void *v, const int32_t *idx, const float *lambda, void *out,
+                           int B, int H, int W, int C, int heads, int n_win, int topk, bra_dtype dtype, void *stream)
+{
+    bra::Geometry g;
+    bra_status s = check_diff(B, H, W, C, heads, n_win, topk, dtype, false, &g);
+    if (s != BRA_OK) return s;
+    if (B == 0) return BRA_OK;
+    if ((s = check_data_ptrs(q, k, v, idx, out)) != BRA_OK) return s;
+    if (!lambda || !aligned(lambda, 4)) return BRA_ERR_INVALID_ARG;
+    return diff_attend_impl(q, k, v, idx, lambda, out, g, dtype, static_cast<cudaStream_t>(stream));
+}
+
+bra_status bra_forward_diff(const void *q, const void *k, const void *v, int32_t *idx, const float *lambda, void *out,
+                            int B, int H, int W, int C, int heads, int n_win, int topk, bra_dtype dtype, void *stream)
+{
+    bra::Geometry g;
+    bra_status s = check_diff(B, H, W, C, heads, n_win, topk, dtype, n_win != 1, &g);
+    if (s != BRA_OK) return s;
+    if (B == 0) return BRA_OK;
+    if ((s = check_data_ptrs(q, k, v, idx, out)) != BRA_OK) return s;
+    if (!lambda || !aligned(lambda, 4)) return BRA_ERR_INVALID_ARG;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (g.R == 1) {  // one region routes to itself whatever its affinity
+        const cudaError_t e = cudaMemsetAsync(idx, 0, (size_t)B * sizeof(int32_t), cs);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(idx)");
+    } else {
+        const size_t out_bytes = (size_t)B * H * W * C * (dtype == BRA_BF16 ? 2 : 4);
+        if ((s = route_impl(q, k, idx, g, dtype, cs, out, out_bytes)) != BRA_OK) return s;
+    }
+    return diff_attend_impl(q, k, v, idx, lambda, out, g, dtype, cs);
+}
+
+bra_status bra_diff_attend_backward(const void *q, const void *k, const void *v, const int32_t *idx, const float *lambda,
+                                    const void *dout, void *dq, void *dk, void *dv, float *dlambda, int B, int H, int W,
+                                    int C, int heads, int n_win, int topk, bra_dtype dtype, void *stream)
+{
+    bra::Geometry g;
+    bra_status s = check_diff(B, H, W, C, heads, n_win, topk, dtype, false, &g);
+    if (s != BRA_OK) return s;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (B == 0) {  // no image, no gradient: dlambda is an empty sum
+        if (!dlambda) return BRA_OK;
+        const cudaError_t e = cudaMemsetAsync(dlambda, 0, (size_t)heads * sizeof(float), cs);
+        return e == cudaSuccess ? BRA_OK : cuda_fail(e, "cudaMemsetAsync(dlambda)");
+    }
+    if ((s = check_data_ptrs(q, k, v, idx, dout)) != BRA_OK) return s;
+    if (!lambda || !dq || !dk || !dv || !dlambda || !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) ||
+        !aligned(lambda, 4) || !aligned(dlambda, 4))
+        return BRA_ERR_INVALID_ARG;
+    // the queries that meet one region are numbered in 31 bits
+    if ((long long)g.N * topk > (1LL << 30)) return BRA_ERR_UNSUPPORTED;
+    DeviceState *st = nullptr;
+    if ((s = device_state(&st)) != BRA_OK) return s;
+    const bool bf16 = dtype == BRA_BF16, mma = bf16 && bra::diff_mma_supports(g);
+    bra::DiffArgs a = {};
+    bra::diff_plan(a, g);
+    const size_t stats = (size_t)B * heads * g.N * sizeof(float4);
+    const size_t parts = ((size_t)heads * bra::diff_backward_parts(g, mma) * sizeof(float) + 15) & ~(size_t)15;
+    const size_t list = ((size_t)B * g.R * topk * sizeof(int32_t) + 15) & ~(size_t)15;
+    const size_t start = (size_t)B * (g.R + 1) * sizeof(int32_t);
+    uint8_t *ws = nullptr;
+    cudaError_t e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), stats + parts + list + start, st->pool, cs);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMallocFromPoolAsync(differential backward scratch)");
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.dout = dout;
+    a.idx = idx;
+    a.lam = lambda;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.dlam = dlambda;
+    a.err = st->error_word;
+    a.stats = reinterpret_cast<float4 *>(ws);
+    a.dlam_part = reinterpret_cast<float *>(ws + stats);
+    int32_t *wlist = reinterpret_cast<int32_t *>(ws + stats + parts);
+    int32_t *wstart = reinterpret_cast<int32_t *>(ws + stats + parts + list);
+    a.list = wlist;
+    a.start = wstart;
+    e = bra::launch_diff_invert(a, wlist, wstart, cs);
+    if (e == cudaSuccess)
+        e = mma ? bra::launch_diff_backward_mma(a, cs) : bra::launch_diff_simt(a, true, bf16, cs);
+    const cudaError_t f = cudaFreeAsync(ws, cs);
+    if (e != cudaSuccess) return cuda_fail(e, "differential backward kernels");
+    if (f != cudaSuccess) return cuda_fail(f, "cudaFreeAsync(differential backward scratch)");
+    return BRA_OK;
+}
+
+// ---------------------------------------------------------------- rotary positions
+
+// Whether [p, p + bytes) and [r, r + bytes) share memory without being the same buffer.
+static bool overlaps(const void *p, const void *r, size_t bytes)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(r);
+    return x != y && (x < y ? y - x : x - y) < bytes;
+}
+
+bra_status bra_rope(const void *q, const void *k, void *q_out, void *k_out, const float *freqs, const int32_t *positions,
+                    int64_t y0, int64_t x0, int B, int H, int W, int C, int heads, int n, int axes, int interleaved,
+                    int inverse, float mscale, bra_dtype dtype, void *stream)
+{
+    if (dtype != BRA_F32 && dtype != BRA_BF16) return BRA_ERR_INVALID_ARG;
+    if (B < 0 || H <= 0 || W <= 0 || C <= 0 || heads <= 0 || n <= 0 || (axes != 1 && axes != 2)) return BRA_ERR_INVALID_ARG;
+    if (C % heads != 0 || (C / heads) % 2 != 0 || 2LL * axes * n > C / heads) return BRA_ERR_INVALID_ARG;
+    const int elem = dtype == BRA_BF16 ? 2 : 4;
+    if (((long long)C * elem) % 16 != 0) return BRA_ERR_INVALID_ARG;
+    constexpr int64_t kFar = (int64_t)1 << 31;
+    if (y0 < -kFar || y0 > kFar || x0 < -kFar || x0 > kFar) return BRA_ERR_INVALID_ARG;
+    if (B == 0) return BRA_OK;
+    if (!q || !q_out || !freqs || (!k != !k_out)) return BRA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) || !aligned(freqs, 4) ||
+        !aligned(positions, 4))
+        return BRA_ERR_INVALID_ARG;
+    if ((long long)H * W > 0x7fffffffLL / 2) return BRA_ERR_UNSUPPORTED;
+    // in place is the same buffer; outputs that lie elsewhere share nothing with an input or each other
+    const size_t bytes = (size_t)B * H * W * C * elem;
+    if (overlaps(q, q_out, bytes)) return BRA_ERR_INVALID_ARG;
+    if (k && (overlaps(k, k_out, bytes) || q_out == k_out || overlaps(q_out, k_out, bytes) || q_out == k ||
+              overlaps(q_out, k, bytes) || k_out == q || overlaps(k_out, q, bytes)))
+        return BRA_ERR_INVALID_ARG;
+    DeviceState *st = nullptr;
+    const bra_status s = device_state(&st);
+    if (s != BRA_OK) return s;
+    bra::RopeArgs a = {};
+    a.q = q;
+    a.k = k;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.freqs = freqs;
+    a.pos = positions;
+    a.y0 = y0;
+    a.x0 = x0;
+    a.B = B;
+    a.H = H;
+    a.W = W;
+    a.C = C;
+    a.heads = heads;
+    a.hd = C / heads;
+    a.n = n;
+    a.axes = axes;
+    a.tensors = k ? 2 : 1;
+    a.mscale = mscale;
+    a.interleaved = interleaved != 0;
+    a.inverse = inverse != 0;
+    const cudaError_t e = bra::launch_rope(a, dtype == BRA_BF16, st->num_sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? BRA_OK : cuda_fail(e, "rotary position kernel");
+}
+
+// ---------------------------------------------------------------- norms around a block
+
+// The checks and the arguments both passes share. gate_images: 0 no gate, 1 a gate [C], B a gate [B, C].
+static bra_status norm_args(bra::NormArgs *a, const void *x, const void *h, const float *gate, int gate_images,
+                            const float *post_w, const float *post_b, const float *pre_w, const float *pre_b, float alpha,
+                            float eps, int kind, int B, int H, int W, int C, bra_dtype dtype)
+{
+    if (dtype != BRA_F32 && dtype != BRA_BF16) return BRA_ERR_INVALID_ARG;
+    if (B < 0 || H <= 0 || W <= 0 || C <= 0 || (kind != BRA_NORM_LAYER && kind != BRA_NORM_RMS)) return BRA_ERR_INVALID_ARG;
+    if (!(eps >= 0.f)) return BRA_ERR_INVALID_ARG;
+    if (((long long)C * (dtype == BRA_BF16 ? 2 : 4)) % 16 != 0) return BRA_ERR_INVALID_ARG;
+    if (!h && (gate || post_w)) return BRA_ERR_INVALID_ARG;          // nothing to gate or normalise
+    if ((!post_w && post_b) || (!pre_w && pre_b)) return BRA_ERR_INVALID_ARG;  // a bias belongs to its weight
+    if (!h && !pre_w) return BRA_ERR_INVALID_ARG;                     // nothing to do
+    if (gate ? (gate_images != 1 && gate_images != B) : gate_images != 0) return BRA_ERR_INVALID_ARG;
+    if (!bra::norm_supports(C, dtype == BRA_BF16)) return BRA_ERR_UNSUPPORTED;
+    const long long rows = (long long)H * W;
+    const bool own = gate && gate_images > 1;
+    if (rows > 0x7fffffffLL / 2 || (!own && rows * B > 0x7fffffffLL / 2)) return BRA_ERR_UNSUPPORTED;
+    if (B == 0) return BRA_OK;
+    if (!x || !aligned(x, 16) || !aligned(h, 16) || !aligned(gate, 16) || !aligned(post_w, 16) || !aligned(post_b, 16) ||
+        !aligned(pre_w, 16) || !aligned(pre_b, 16))
+        return BRA_ERR_INVALID_ARG;
+    a->x = x;
+    a->h = h;
+    a->gate = gate;
+    a->post_w = post_w;
+    a->post_b = post_b;
+    a->pre_w = pre_w;
+    a->pre_b = pre_b;
+    a->gate_images = own;
+    a->images = own ? B : 1;
+    a->rows = (int)(own ? rows : rows * B);
+    a->C = C;
+    a->nvec = C / (dtype == BRA_BF16 ? 8 : 4);
+    a->layer = kind == BRA_NORM_LAYER;
+    a->alpha = alpha;
+    a->eps = eps;
+    a->inv_c = 1.f / (float)C;
+    return BRA_OK;
+}
+
+bra_status bra_norm_residual(const void *x, const void *h, const float *gate, int gate_images, const float *post_weight,
+                             const float *post_bias, const float *pre_weight, const float *pre_bias, float alpha, float eps,
+                             bra_norm_kind kind, void *s_out, void *y_out, int B, int H, int W, int C, bra_dtype dtype,
+                             void *stream)
+{
+    bra::NormArgs a = {};
+    bra_status s = norm_args(&a, x, h, gate, gate_images, post_weight, post_bias, pre_weight, pre_bias, alpha, eps, kind, B,
+                             H, W, C, dtype);
+    if (s != BRA_OK || B == 0) return s;
+    if ((h && !s_out) || (!!pre_weight != !!y_out) || !aligned(s_out, 16) || !aligned(y_out, 16)) return BRA_ERR_INVALID_ARG;
+    const size_t bytes = (size_t)B * H * W * C * (dtype == BRA_BF16 ? 2 : 4);
+    // a row is read whole before it is written: an output may be x or h itself, not a part of them
+    for (const void *out : {(const void *)s_out, (const void *)y_out})
+        if (out && (overlaps(out, x, bytes) || (h && overlaps(out, h, bytes)))) return BRA_ERR_INVALID_ARG;
+    if (s_out && y_out && (s_out == y_out || overlaps(s_out, y_out, bytes))) return BRA_ERR_INVALID_ARG;
+    DeviceState *st = nullptr;
+    if ((s = device_state(&st)) != BRA_OK) return s;
+    a.s = s_out;
+    a.y = y_out;
+    bra::norm_plan(a, false, st->num_sms);
+    const cudaError_t e = bra::launch_norm_residual(a, dtype == BRA_BF16, false, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? BRA_OK : cuda_fail(e, "norm kernel");
+}
+
+bra_status bra_norm_residual_backward(const void *x, const void *h, const void *dy, const void *ds, const float *gate,
+                                      int gate_images, const float *post_weight, const float *post_bias,
+                                      const float *pre_weight, const float *pre_bias, float alpha, float eps,
+                                      bra_norm_kind kind, void *dx, void *dh, float *dgate, float *dpost_weight,
+                                      float *dpost_bias, float *dpre_weight, float *dpre_bias, int B, int H, int W, int C,
+                                      bra_dtype dtype, void *stream)
+{
+    bra::NormArgs a = {};
+    bra_status s = norm_args(&a, x, h, gate, gate_images, post_weight, post_bias, pre_weight, pre_bias, alpha, eps, kind, B,
+                             H, W, C, dtype);
+    if (s != BRA_OK) return s;
+    if (!!gate != !!dgate || !!post_weight != !!dpost_weight || !!post_bias != !!dpost_bias ||
+        !!pre_weight != !!dpre_weight || !!pre_bias != !!dpre_bias || !aligned(dgate, 4) || !aligned(dpost_weight, 4) ||
+        !aligned(dpost_bias, 4) || !aligned(dpre_weight, 4) || !aligned(dpre_bias, 4))
+        return BRA_ERR_INVALID_ARG;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (B == 0) {  // empty sums; a gate of its own for each of no images has no gradient
+        cudaError_t e = cudaSuccess;
+        for (float *p : {gate_images == 1 ? dgate : nullptr, dpost_weight, dpost_bias, dpre_weight, dpre_bias})
+            if (p && e == cudaSuccess) e = cudaMemsetAsync(p, 0, (size_t)C * sizeof(float), cs);
+        return e == cudaSuccess ? BRA_OK : cuda_fail(e, "cudaMemsetAsync(weight gradients)");
+    }
+    if (!dx || (!!h != !!dh) || (!!pre_weight != !!dy) || (!dy && !ds) || !aligned(dx, 16) || !aligned(dh, 16) ||
+        !aligned(dy, 16) || !aligned(ds, 16))
+        return BRA_ERR_INVALID_ARG;
+    const size_t bytes = (size_t)B * H * W * C * (dtype == BRA_BF16 ? 2 : 4);
+    for (const void *out : {(const void *)dx, (const void *)dh})
+        for (const void *in : {x, h, dy, ds})
+            if (out && in && overlaps(out, in, bytes)) return BRA_ERR_INVALID_ARG;
+    if (dh && (dx == dh || overlaps(dx, dh, bytes))) return BRA_ERR_INVALID_ARG;
+    DeviceState *st = nullptr;
+    if ((s = device_state(&st)) != BRA_OK) return s;
+    a.dy = dy;
+    a.ds = ds;
+    a.dx = dx;
+    a.dh = dh;
+    a.dgate = dgate;
+    a.dpost_w = dpost_weight;
+    a.dpost_b = dpost_bias;
+    a.dpre_w = dpre_weight;
+    a.dpre_b = dpre_bias;
+    bra::norm_plan(a, true, st->num_sms);
+    void *part = nullptr;
+    cudaError_t e = cudaMallocFromPoolAsync(&part, (size_t)a.units * 5 * C * sizeof(float), st->pool, cs);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMallocFromPoolAsync(column sums)");
+    a.part = static_cast<float *>(part);
+    e = bra::launch_norm_residual(a, dtype == BRA_BF16, true, cs);
+    const cudaError_t f = cudaFreeAsync(part, cs);
+    if (e != cudaSuccess) return cuda_fail(e, "norm backward kernels");
+    if (f != cudaSuccess) return cuda_fail(f, "cudaFreeAsync(column sums)");
+    return BRA_OK;
 }
 
 bra_status bra_selftest_wait_timeout(unsigned limit_us, void *stream)

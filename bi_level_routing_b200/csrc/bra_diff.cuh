@@ -1,0 +1,161 @@
+// bra_diff.cuh -- what the differential attention kernels share: the call's geometry, the gather of
+// a region's routed token rows, and the tile pieces of the bf16 tensor-core kernels.
+//
+// Differential attention. Head h owns hd = C / heads channels of q, k, v and out. The first d = hd / 2
+// channels of its q and k make map 1, the last d map 2; v keeps all hd. For a query of region r, over
+// the tokens j of the regions idx[b, r, :],
+//   out = (softmax_j(d^-1/2 q1 . k1_j) - lam[h] softmax_j(d^-1/2 q2 . k2_j)) v_j.
+// With P1, P2 the two maps, dP = dout V^T and D_i = rowsum(P_i dP) the gradients of sum(dout out) are
+//   dS1 = d^-1/2 P1 (dP - D1),  dS2 = -lam d^-1/2 P2 (dP - D2),
+//   dq_i = dS_i k_i,  dk_i = dS_i^T q_i,  dv = (P1 - lam P2)^T dout,  dlam = -sum over queries of D2.
+#pragma once
+
+#include "bra_device.cuh"
+#include "bra_launch.h"
+
+namespace bra {
+
+// Division of 0 <= n < 2^31 by a fixed d >= 1 as a multiplication and a shift: with
+// l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1, n / d = (hi32(n m) + n) >> l.
+struct FastDiv {
+    uint32_t m, l;
+    int d;
+    __host__ static FastDiv of(int d)
+    {
+        uint32_t l = 0;
+        while ((1ull << l) < (uint64_t)d) ++l;
+        FastDiv f;
+        f.m = (uint32_t)(((1ull << 32) * ((1ull << l) - (uint64_t)d)) / (uint64_t)d + 1);
+        f.l = l;
+        f.d = d;
+        return f;
+    }
+    __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, m) + (uint32_t)n) >> l); }
+    __device__ __forceinline__ void divmod(int n, int &q, int &r) const
+    {
+        q = div(n);
+        r = n - q * d;
+    }
+};
+
+struct DiffArgs {
+    const void *q, *k, *v, *dout;
+    const int32_t *idx;
+    const float *lam;
+    void *out;
+    void *dq, *dk, *dv;     // of the input type
+    float *dlam;            // [heads]
+    float4 *stats;          // [B, heads, N]: L1, L2 (log2 of each map's normaliser), D1, D2
+    float *dlam_part;       // [heads, nparts]: sums of D2, one for each (image, region, query tile, warp)
+    const int32_t *list;    // [B, R * topk]: for each region, the regions that route to it, in order
+    const int32_t *start;   // [B, R + 1]: where each region's part of the list starts
+    unsigned *err;
+    int B, H, W, C, heads, hd, d, n_win, hr, wr, rs, R, topk, N;
+    int tiles;      // tiles of a region's tokens
+    int nitems;     // work items of the launch
+    int nparts;
+    float scale;        // d^-1/2
+    float scale_log2;   // d^-1/2 log2(e)
+    FastDiv by_rs, by_wr, by_nwin, by_heads, by_tiles, by_R;
+};
+
+// Offset y W + x (in tokens, inside an image) of token `tok` of the region whose first token lies at
+// `base`.
+__device__ __forceinline__ int token_at(const DiffArgs &a, int base, int tok)
+{
+    int y, x;
+    a.by_wr.divmod(tok, y, x);
+    return base + y * a.W + x;
+}
+
+// Offset of region s's first token.
+__device__ __forceinline__ int region_at(const DiffArgs &a, int s)
+{
+    int ry, rx;
+    a.by_nwin.divmod(s, ry, rx);
+    return ry * a.hr * a.W + rx * a.wr;
+}
+
+// One item of a launch: heads fastest (neighbouring heads' channels share cache lines), then the
+// tiles of a region, the regions, the images.
+struct DiffItem {
+    int h, t, r, b;
+};
+__device__ __forceinline__ DiffItem diff_item(const DiffArgs &a, int item)
+{
+    DiffItem it;
+    int rest;
+    a.by_heads.divmod(item, rest, it.h);
+    a.by_tiles.divmod(rest, rest, it.t);
+    a.by_R.divmod(rest, it.b, it.r);
+    return it;
+}
+
+// A warp writes the first-token offsets of the valid regions of idx[b, r, :] to `bases`, in order,
+// and returns how many there are; entries outside [0, R) are left out and flagged.
+__device__ __forceinline__ int gather_bases(const DiffArgs &a, const int32_t *row, int *bases, int lane)
+{
+    int n = 0;
+    for (int j0 = 0; j0 < a.topk; j0 += 32) {
+        const int j = j0 + lane;
+        const int s = j < a.topk ? __ldg(row + j) : 0;
+        const bool ok = j < a.topk && s >= 0 && s < a.R;
+        if (j < a.topk && !ok) flag_error(a.err, kErrIndex);
+        const unsigned mask = __ballot_sync(0xffffffffu, ok);
+        if (ok) bases[n + __popc(mask & ((1u << lane) - 1u))] = region_at(a, s);
+        n += __popc(mask);
+    }
+    return n;
+}
+
+// A 16-byte asynchronous copy, or 16 zero bytes when `real` is false (src is not read then).
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool real)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+template <int N> __device__ __forceinline__ void cp_async_wait_but()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The new running maximum. While every score so far is -inf it is 0, so that exp2(score - max) is 0,
+// not NaN, and later tiles decide.
+__device__ __forceinline__ float finite_max(float before, float top)
+{
+    const float m = fmaxf(before, top);
+    return m == -INFINITY ? 0.f : m;
+}
+
+__device__ __forceinline__ float quad_max(float x)
+{
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+__device__ __forceinline__ float quad_sum(float x)
+{
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+__device__ __forceinline__ float warp_sum(float x)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+__device__ __forceinline__ float warp_max(float x)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+
+// The barrier of one group of WPI warps of a 4-warp CTA.
+template <int WPI> __device__ __forceinline__ void group_barrier(int group)
+{
+    if (WPI == 1)
+        __syncwarp();
+    else
+        named_barrier(1 + group, 32 * WPI);
+}
+
+}  // namespace bra

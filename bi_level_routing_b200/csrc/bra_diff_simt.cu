@@ -1,0 +1,518 @@
+// bra_diff_simt.cu -- differential attention and its gradients on CUDA cores (formula in
+// bra_diff.cuh): fp32 maps, and bf16 heads whose halves are not whole 16-byte chunks. fp32
+// throughout, hd a multiple of 8 up to 128, regions of any size.
+//
+// A CTA owns WARPS x RW token rows of one (image, region, head), RW of them a warp's; the tokens they
+// meet (keys for the forward pass and dq, queries for dk and dv) come through shared memory in tiles of
+// 64, two to a lane. Scores: a lane holds two rows of the tile against the warp's RW rows, whose
+// channels are read as broadcasts (RW + 8 shared-memory wavefronts for 8 RW FMAs of a warp, so the
+// FMA pipe is the bound from RW = 8 on). The products with the tile's channels turn round: lanes
+// over channels, the probabilities of four tile rows read as one broadcast.
+// As in bra_diff_backward.cu, nothing is added in memory.
+#include "bra_diff.cuh"
+
+namespace bra {
+
+namespace {
+
+constexpr int kTileRows = 64;
+
+template <int WARPS, int RW> struct SimtTile {
+    static constexpr int kRows = WARPS * RW;
+    // floats of shared memory: two tiles, two sets of own rows, NP score planes of each warp
+    static size_t floats(int hd, int own, int planes)
+    {
+        return (size_t)(2 * kTileRows + own * kRows) * (hd + 4) + (size_t)WARPS * planes * RW * kTileRows;
+    }
+};
+
+// Row `row` of a [rows][hd + 4] fp32 tile from the hd channels at src (16-byte vectors), or zeros.
+template <typename T>
+__device__ __forceinline__ void stage_vector(float *tile, int hd, int row, int u, const T *src, bool real)
+{
+    constexpr int V = Vec16<T>::N;
+    float f[V];
+    if (real) {
+        Vec16<T>::load(src + u * V, f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = 0.f;
+    }
+    float4 *dst = reinterpret_cast<float4 *>(tile + row * (hd + 4) + u * V);
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) dst[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+}
+
+// acc[i][0..1] += rows[i] . tile[lane], tile[lane + 32] over channels [c0, c1)
+template <int RW>
+__device__ __forceinline__ void lane_products(float (&acc)[RW][2], const float *rows, const float *tile, int hd, int lane,
+                                              int c0, int c1)
+{
+    const float *t0 = tile + lane * (hd + 4), *t1 = t0 + 32 * (hd + 4);
+#pragma unroll 1
+    for (int c = c0; c < c1; c += 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(t0 + c), y = *reinterpret_cast<const float4 *>(t1 + c);
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+            const float4 q = *reinterpret_cast<const float4 *>(rows + i * (hd + 4) + c);
+            acc[i][0] = fmaf(q.x, x.x, fmaf(q.y, x.y, fmaf(q.z, x.z, fmaf(q.w, x.w, acc[i][0]))));
+            acc[i][1] = fmaf(q.x, y.x, fmaf(q.y, y.y, fmaf(q.z, y.z, fmaf(q.w, y.w, acc[i][1]))));
+        }
+    }
+}
+
+// o[i][cc] += sum over the tile's rows j of p[i][j] tile[j][lane + 32 cc]; p of channel c is pa for
+// c < split, else pb
+template <int RW, int NC>
+__device__ __forceinline__ void turn_products(float (&o)[RW][NC], const float *pa, const float *pb, int split,
+                                              const float *tile, int hd, int lane)
+{
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc) {
+        const int c = min(lane + 32 * cc, hd - 1);
+        const float *p = c < split ? pa : pb;
+#pragma unroll 1
+        for (int j = 0; j < kTileRows; j += 4) {
+            const float v0 = tile[j * (hd + 4) + c], v1 = tile[(j + 1) * (hd + 4) + c];
+            const float v2 = tile[(j + 2) * (hd + 4) + c], v3 = tile[(j + 3) * (hd + 4) + c];
+#pragma unroll
+            for (int i = 0; i < RW; ++i) {
+                const float4 w = *reinterpret_cast<const float4 *>(p + i * kTileRows + j);
+                o[i][cc] = fmaf(w.x, v0, fmaf(w.y, v1, fmaf(w.z, v2, fmaf(w.w, v3, o[i][cc]))));
+            }
+        }
+    }
+}
+
+template <int RW, int M> __device__ __forceinline__ void clear(float (&x)[RW][M])
+{
+#pragma unroll
+    for (int i = 0; i < RW; ++i)
+#pragma unroll
+        for (int j = 0; j < M; ++j) x[i][j] = 0.f;
+}
+
+}  // namespace
+
+template <typename T, int WARPS, int RW, int NC>
+__global__ void __launch_bounds__(32 * WARPS) diff_attend_simt_kernel(const DiffArgs a)
+{
+    constexpr int ROWS = WARPS * RW, THREADS = 32 * WARPS;
+    extern __shared__ float4 smem4[];
+    const int hd = a.hd, stride = hd + 4, nvec = hd / Vec16<T>::N;
+    float *sk = reinterpret_cast<float *>(smem4), *sv = sk + kTileRows * stride, *sq = sv + kTileRows * stride;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float *sp = sq + ROWS * stride + warp * 2 * RW * kTileRows;  // [map][RW][64]
+    int *count = reinterpret_cast<int *>(sq + ROWS * stride + WARPS * 2 * RW * kTileRows);
+    int *bases = count + 4;
+    const DiffItem it = diff_item(a, blockIdx.x);
+    const int64_t image = (int64_t)it.b * a.N * a.C + it.h * hd;
+    const T *gq = static_cast<const T *>(a.q) + image, *gk = static_cast<const T *>(a.k) + image;
+    const T *gv = static_cast<const T *>(a.v) + image;
+    const int region = region_at(a, it.r);
+    grid_dependency_wait();
+    if (warp == 0) {
+        const int n = gather_bases(a, a.idx + ((int64_t)it.b * a.R + it.r) * a.topk, bases, lane);
+        if (lane == 0) *count = n;
+    }
+    for (int e = threadIdx.x; e < ROWS * nvec; e += THREADS) {
+        const int row = e / nvec, tok = it.t * ROWS + row;
+        const bool in = tok < a.rs;
+        stage_vector<T>(sq, hd, row, e % nvec, gq + (int64_t)(in ? token_at(a, region, tok) : 0) * a.C, in);
+    }
+    __syncthreads();
+    const int nkeys = *count * a.rs;
+    const float *rows = sq + warp * RW * stride;
+    const bool busy = it.t * ROWS + warp * RW < a.rs;  // the warp has a row
+
+    float o[2][RW][NC], mx[2][RW], l[2][RW];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        clear<RW, NC>(o[m]);
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+            mx[m][i] = -INFINITY;
+            l[m][i] = 0.f;
+        }
+    }
+    for (int k0 = 0; k0 < nkeys; k0 += kTileRows) {
+        if (k0) __syncthreads();
+        for (int e = threadIdx.x; e < kTileRows * nvec; e += THREADS) {
+            const int row = e / nvec, key = k0 + row;
+            const bool real = key < nkeys;
+            int64_t off = 0;
+            if (real) {
+                int slot, tok;
+                a.by_rs.divmod(key, slot, tok);
+                off = (int64_t)token_at(a, bases[slot], tok) * a.C;
+            }
+            stage_vector<T>(sk, hd, row, e % nvec, gk + off, real);
+            stage_vector<T>(sv, hd, row, e % nvec, gv + off, real);
+        }
+        __syncthreads();
+        if (!busy) continue;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            float s[RW][2];
+            clear<RW, 2>(s);
+            lane_products<RW>(s, rows, sk, hd, lane, m * a.d, (m + 1) * a.d);
+#pragma unroll
+            for (int i = 0; i < RW; ++i) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    if (k0 + lane + 32 * x >= nkeys) s[i][x] = -INFINITY;
+                const float mn = finite_max(mx[m][i], warp_max(fmaxf(s[i][0], s[i][1])) * a.scale_log2);
+                const float corr = exp2f(mx[m][i] - mn);
+                mx[m][i] = mn;
+                const float e0 = exp2f(fmaf(s[i][0], a.scale_log2, -mn)), e1 = exp2f(fmaf(s[i][1], a.scale_log2, -mn));
+                l[m][i] = l[m][i] * corr + (e0 + e1);
+                sp[(m * RW + i) * kTileRows + lane] = e0;
+                sp[(m * RW + i) * kTileRows + lane + 32] = e1;
+#pragma unroll
+                for (int cc = 0; cc < NC; ++cc) o[m][i][cc] *= corr;
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+            turn_products<RW, NC>(o[m], sp + m * RW * kTileRows, nullptr, hd, sv, hd, lane);
+        __syncwarp();
+    }
+    if (!busy) return;
+    const float lam = __ldg(a.lam + it.h);
+    T *out = static_cast<T *>(a.out) + image;
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+        const int tok = it.t * ROWS + warp * RW + i;
+        if (tok >= a.rs) break;
+        const float l1 = warp_sum(l[0][i]), l2 = warp_sum(l[1][i]);
+        const float w1 = l1 > 0.f ? 1.f / l1 : 0.f, w2 = l2 > 0.f ? -lam / l2 : 0.f;
+        T *dst = out + (int64_t)token_at(a, region, tok) * a.C;
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) {
+            const int c = lane + 32 * cc;
+            if (c < hd) dst[c] = from_float<T>(fmaf(o[0][i][cc], w1, o[1][i][cc] * w2));
+        }
+    }
+}
+
+// dq and the statistics (see bra_diff_backward.cu)
+template <typename T, int WARPS, int RW, int NC>
+__global__ void __launch_bounds__(32 * WARPS) diff_backward_queries_simt_kernel(const DiffArgs a)
+{
+    constexpr int ROWS = WARPS * RW, THREADS = 32 * WARPS;
+    extern __shared__ float4 smem4[];
+    const int hd = a.hd, stride = hd + 4, nvec = hd / Vec16<T>::N;
+    float *sk = reinterpret_cast<float *>(smem4), *sv = sk + kTileRows * stride, *sq = sv + kTileRows * stride;
+    float *sd = sq + ROWS * stride;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float *sp = sd + ROWS * stride + warp * 2 * RW * kTileRows;
+    int *count = reinterpret_cast<int *>(sd + ROWS * stride + WARPS * 2 * RW * kTileRows);
+    int *bases = count + 4;
+    const DiffItem it = diff_item(a, blockIdx.x);
+    const int64_t image = (int64_t)it.b * a.N * a.C + it.h * hd;
+    const T *gq = static_cast<const T *>(a.q) + image, *gk = static_cast<const T *>(a.k) + image;
+    const T *gv = static_cast<const T *>(a.v) + image, *gd = static_cast<const T *>(a.dout) + image;
+    const int region = region_at(a, it.r);
+    grid_dependency_wait();
+    if (warp == 0) {
+        const int n = gather_bases(a, a.idx + ((int64_t)it.b * a.R + it.r) * a.topk, bases, lane);
+        if (lane == 0) *count = n;
+    }
+    for (int e = threadIdx.x; e < ROWS * nvec; e += THREADS) {
+        const int row = e / nvec, tok = it.t * ROWS + row;
+        const bool in = tok < a.rs;
+        const int64_t off = (int64_t)(in ? token_at(a, region, tok) : 0) * a.C;
+        stage_vector<T>(sq, hd, row, e % nvec, gq + off, in);
+        stage_vector<T>(sd, hd, row, e % nvec, gd + off, in);
+    }
+    __syncthreads();
+    const int nkeys = *count * a.rs;
+    const float *rows = sq + warp * RW * stride, *drows = sd + warp * RW * stride;
+    const bool busy = it.t * ROWS + warp * RW < a.rs;
+
+    auto stage = [&](int k0) {
+        for (int e = threadIdx.x; e < kTileRows * nvec; e += THREADS) {
+            const int row = e / nvec, key = k0 + row;
+            const bool real = key < nkeys;
+            int64_t off = 0;
+            if (real) {
+                int slot, tok;
+                a.by_rs.divmod(key, slot, tok);
+                off = (int64_t)token_at(a, bases[slot], tok) * a.C;
+            }
+            stage_vector<T>(sk, hd, row, e % nvec, gk + off, real);
+            stage_vector<T>(sv, hd, row, e % nvec, gv + off, real);
+        }
+    };
+    float mx[2][RW], l[2][RW], ed[2][RW];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+            mx[m][i] = -INFINITY;
+            l[m][i] = ed[m][i] = 0.f;
+        }
+    for (int k0 = 0; k0 < nkeys; k0 += kTileRows) {
+        if (k0) __syncthreads();
+        stage(k0);
+        __syncthreads();
+        if (!busy) continue;
+        float dp[RW][2];
+        clear<RW, 2>(dp);
+        lane_products<RW>(dp, drows, sv, hd, lane, 0, hd);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            float s[RW][2];
+            clear<RW, 2>(s);
+            lane_products<RW>(s, rows, sk, hd, lane, m * a.d, (m + 1) * a.d);
+#pragma unroll
+            for (int i = 0; i < RW; ++i) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    if (k0 + lane + 32 * x >= nkeys) s[i][x] = -INFINITY;
+                const float mn = finite_max(mx[m][i], warp_max(fmaxf(s[i][0], s[i][1])) * a.scale_log2);
+                const float corr = exp2f(mx[m][i] - mn);
+                mx[m][i] = mn;
+                const float e0 = exp2f(fmaf(s[i][0], a.scale_log2, -mn)), e1 = exp2f(fmaf(s[i][1], a.scale_log2, -mn));
+                l[m][i] = l[m][i] * corr + (e0 + e1);
+                ed[m][i] = ed[m][i] * corr + fmaf(e0, dp[i][0], e1 * dp[i][1]);
+            }
+        }
+    }
+    float Ls[2][RW], D[2][RW], dsum = 0.f;
+    float4 *stats = a.stats + ((int64_t)it.b * a.heads + it.h) * a.N;
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const float sum = warp_sum(l[m][i]), num = warp_sum(ed[m][i]);
+            Ls[m][i] = sum > 0.f ? mx[m][i] + log2f(sum) : INFINITY;
+            D[m][i] = sum > 0.f ? num / sum : 0.f;
+        }
+        const int tok = it.t * ROWS + warp * RW + i;
+        if (tok < a.rs) {
+            if (lane == 0) stats[token_at(a, region, tok)] = make_float4(Ls[0][i], Ls[1][i], D[0][i], D[1][i]);
+            dsum += D[1][i];
+        }
+    }
+    if (lane == 0)
+        a.dlam_part[(int64_t)it.h * a.nparts + (((int64_t)it.b * a.R + it.r) * a.tiles + it.t) * WARPS + warp] = dsum;
+
+    float dq[RW][NC];
+    clear<RW, NC>(dq);
+    for (int k0 = 0; k0 < nkeys; k0 += kTileRows) {
+        if (nkeys > kTileRows) {  // else the only tile is still in place
+            __syncthreads();
+            stage(k0);
+            __syncthreads();
+        }
+        if (!busy) continue;
+        float dp[RW][2];
+        clear<RW, 2>(dp);
+        lane_products<RW>(dp, drows, sv, hd, lane, 0, hd);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            float s[RW][2];
+            clear<RW, 2>(s);
+            lane_products<RW>(s, rows, sk, hd, lane, m * a.d, (m + 1) * a.d);
+#pragma unroll
+            for (int i = 0; i < RW; ++i)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float p = exp2f(fmaf(s[i][x], a.scale_log2, -Ls[m][i]));
+                    sp[(m * RW + i) * kTileRows + lane + 32 * x] =
+                        k0 + lane + 32 * x < nkeys ? p * (dp[i][x] - D[m][i]) : 0.f;
+                }
+        }
+        __syncwarp();
+        turn_products<RW, NC>(dq, sp, sp + RW * kTileRows, a.d, sk, hd, lane);
+        __syncwarp();
+    }
+    if (!busy) return;
+    const float s1 = a.scale, s2 = -__ldg(a.lam + it.h) * a.scale;
+    T *out = static_cast<T *>(a.dq) + image;
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+        const int tok = it.t * ROWS + warp * RW + i;
+        if (tok >= a.rs) break;
+        T *dst = out + (int64_t)token_at(a, region, tok) * a.C;
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) {
+            const int c = lane + 32 * cc;
+            if (c < hd) dst[c] = from_float<T>(dq[i][cc] * (c < a.d ? s1 : s2));
+        }
+    }
+}
+
+// dk, dv and dlam (see bra_diff_backward.cu)
+template <typename T, int WARPS, int RW, int NC>
+__global__ void __launch_bounds__(32 * WARPS) diff_backward_keys_simt_kernel(const DiffArgs a)
+{
+    constexpr int ROWS = WARPS * RW, THREADS = 32 * WARPS;
+    extern __shared__ float4 smem4[];
+    const int hd = a.hd, stride = hd + 4, nvec = hd / Vec16<T>::N;
+    float *sq = reinterpret_cast<float *>(smem4), *sd = sq + kTileRows * stride, *sk = sd + kTileRows * stride;
+    float *sv = sk + ROWS * stride;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float *sp = sv + ROWS * stride + warp * 3 * RW * kTileRows;  // [P1 - lam P2, dS1, dS2][RW][64]
+    grid_dependency_wait();
+    if (blockIdx.x < a.heads) {  // dlam of head blockIdx.x, summed in 64 bits in a fixed order
+        double *part = reinterpret_cast<double *>(smem4);
+        const float *src = a.dlam_part + (int64_t)blockIdx.x * a.nparts;
+        double sum = 0.;
+        for (int e = threadIdx.x; e < a.nparts; e += THREADS) sum += (double)__ldcg(src + e);
+        part[threadIdx.x] = sum;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            double all = 0.;
+            for (int e = 0; e < THREADS; ++e) all += part[e];
+            a.dlam[blockIdx.x] = (float)-all;
+        }
+        __syncthreads();
+    }
+    if (blockIdx.x >= a.nitems) return;
+    const DiffItem it = diff_item(a, blockIdx.x);
+    const int64_t image = (int64_t)it.b * a.N * a.C + it.h * hd;
+    const T *gq = static_cast<const T *>(a.q) + image, *gk = static_cast<const T *>(a.k) + image;
+    const T *gv = static_cast<const T *>(a.v) + image, *gd = static_cast<const T *>(a.dout) + image;
+    const float4 *stats = a.stats + ((int64_t)it.b * a.heads + it.h) * a.N;
+    const int region = region_at(a, it.r);
+    const int32_t *start = a.start + (int64_t)it.b * (a.R + 1) + it.r;
+    const int first = __ldg(start);
+    const int nq = (__ldg(start + 1) - first) * a.rs;
+    const int32_t *list = a.list + (int64_t)it.b * a.R * a.topk + first;
+    auto query_at = [&](int query) {
+        int slot, tok;
+        a.by_rs.divmod(query, slot, tok);
+        return token_at(a, region_at(a, __ldg(list + slot)), tok);
+    };
+    for (int e = threadIdx.x; e < ROWS * nvec; e += THREADS) {
+        const int row = e / nvec, tok = it.t * ROWS + row;
+        const bool in = tok < a.rs;
+        const int64_t off = (int64_t)(in ? token_at(a, region, tok) : 0) * a.C;
+        stage_vector<T>(sk, hd, row, e % nvec, gk + off, in);
+        stage_vector<T>(sv, hd, row, e % nvec, gv + off, in);
+    }
+    const float *krows = sk + warp * RW * stride, *vrows = sv + warp * RW * stride;
+    const bool busy = it.t * ROWS + warp * RW < a.rs;
+    const float lam = __ldg(a.lam + it.h);
+    float dk[RW][NC], dv[RW][NC];
+    clear<RW, NC>(dk);
+    clear<RW, NC>(dv);
+    for (int q0 = 0; q0 < nq; q0 += kTileRows) {
+        if (q0) __syncthreads();
+        for (int e = threadIdx.x; e < kTileRows * nvec; e += THREADS) {
+            const int row = e / nvec, query = q0 + row;
+            const bool real = query < nq;
+            const int64_t off = real ? (int64_t)query_at(query) * a.C : 0;
+            stage_vector<T>(sq, hd, row, e % nvec, gq + off, real);
+            stage_vector<T>(sd, hd, row, e % nvec, gd + off, real);
+        }
+        __syncthreads();
+        if (!busy) continue;
+        float4 st[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int query = q0 + lane + 32 * x;
+            st[x] = query < nq ? __ldcg(stats + query_at(query)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float dp[RW][2], s1[RW][2], s2[RW][2];
+        clear<RW, 2>(dp);
+        clear<RW, 2>(s1);
+        clear<RW, 2>(s2);
+        lane_products<RW>(dp, vrows, sd, hd, lane, 0, hd);
+        lane_products<RW>(s1, krows, sq, hd, lane, 0, a.d);
+        lane_products<RW>(s2, krows, sq, hd, lane, a.d, hd);
+#pragma unroll
+        for (int i = 0; i < RW; ++i)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const bool real = q0 + lane + 32 * x < nq;
+                const float p1 = exp2f(fmaf(s1[i][x], a.scale_log2, -st[x].x));
+                const float p2 = exp2f(fmaf(s2[i][x], a.scale_log2, -st[x].y));
+                float *dst = sp + i * kTileRows + lane + 32 * x;
+                dst[0] = real ? fmaf(-lam, p2, p1) : 0.f;
+                dst[RW * kTileRows] = real ? p1 * (dp[i][x] - st[x].z) : 0.f;
+                dst[2 * RW * kTileRows] = real ? p2 * (dp[i][x] - st[x].w) : 0.f;
+            }
+        __syncwarp();
+        turn_products<RW, NC>(dv, sp, nullptr, hd, sd, hd, lane);
+        turn_products<RW, NC>(dk, sp + RW * kTileRows, sp + 2 * RW * kTileRows, a.d, sq, hd, lane);
+        __syncwarp();
+    }
+    if (!busy) return;
+    const float w1 = a.scale, w2 = -lam * a.scale;
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+        const int tok = it.t * ROWS + warp * RW + i;
+        if (tok >= a.rs) break;
+        const int64_t off = image + (int64_t)token_at(a, region, tok) * a.C;
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) {
+            const int c = lane + 32 * cc;
+            if (c < hd) {
+                static_cast<T *>(a.dk)[off + c] = from_float<T>(dk[i][cc] * (c < a.d ? w1 : w2));
+                static_cast<T *>(a.dv)[off + c] = from_float<T>(dv[i][cc]);
+            }
+        }
+    }
+}
+
+namespace {
+
+template <typename K>
+cudaError_t launch_with(K kernel, int grid, int threads, size_t smem, const DiffArgs &a, cudaStream_t stream)
+{
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3(grid), dim3(threads), smem, stream, a);
+}
+
+template <typename T, int WARPS, int RW, int NC> cudaError_t launch_one(DiffArgs &a, bool backward, cudaStream_t stream)
+{
+    using L = SimtTile<WARPS, RW>;
+    a.tiles = (a.rs + L::kRows - 1) / L::kRows;
+    a.by_tiles = FastDiv::of(a.tiles);
+    const long long items = (long long)a.B * a.R * a.tiles * a.heads;
+    if (items * WARPS > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    a.nitems = (int)items;
+    a.nparts = (int)(items / a.heads * WARPS);
+    const size_t tail = 16 + (((size_t)a.topk * 4 + 15) & ~(size_t)15);
+    const int grid = (int)items;
+    if (!backward)
+        return launch_with(diff_attend_simt_kernel<T, WARPS, RW, NC>, grid, 32 * WARPS, 4 * L::floats(a.hd, 1, 2) + tail, a,
+                           stream);
+    const cudaError_t e = launch_with(diff_backward_queries_simt_kernel<T, WARPS, RW, NC>, grid, 32 * WARPS,
+                                      4 * L::floats(a.hd, 2, 2) + tail, a, stream);
+    if (e != cudaSuccess) return e;
+    return launch_with(diff_backward_keys_simt_kernel<T, WARPS, RW, NC>, grid > a.heads ? grid : a.heads, 32 * WARPS,
+                       4 * L::floats(a.hd, 2, 3), a, stream);
+}
+
+template <typename T, int NC> cudaError_t launch_nc(DiffArgs &a, bool backward, cudaStream_t stream)
+{
+    if (a.rs <= 4) return launch_one<T, 4, 1, NC>(a, backward, stream);
+    if (a.rs <= 16) return launch_one<T, 4, 4, NC>(a, backward, stream);
+    return launch_one<T, 8, 8, NC>(a, backward, stream);
+}
+
+template <typename T> cudaError_t launch_t(DiffArgs &a, bool backward, cudaStream_t stream)
+{
+    switch ((a.hd + 31) / 32) {
+    case 1: return launch_nc<T, 1>(a, backward, stream);
+    case 2: return launch_nc<T, 2>(a, backward, stream);
+    case 3: return launch_nc<T, 3>(a, backward, stream);
+    default: return launch_nc<T, 4>(a, backward, stream);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_diff_simt(const DiffArgs &args, bool backward, bool bf16, cudaStream_t stream)
+{
+    DiffArgs a = args;
+    return bf16 ? launch_t<__nv_bfloat16>(a, backward, stream) : launch_t<float>(a, backward, stream);
+}
+
+}  // namespace bra

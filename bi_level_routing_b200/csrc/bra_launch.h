@@ -184,4 +184,55 @@ cudaError_t launch_route_attend_dense(const CUtensorMap &tq, const CUtensorMap &
                                       const CUtensorMap &tout, int32_t *idx, const Geometry &g, unsigned *err,
                                       cudaStream_t stream);
 
+// ---------------------------------------------------------------- differential attention
+
+struct DiffArgs;  // bra_diff.cuh
+
+// Fills what the kernels need besides the pointers of one call. hd even, at most 128.
+void diff_plan(DiffArgs &a, const Geometry &g);
+// The bf16 tensor-core kernels: hd a multiple of 16 up to 128. The CUDA-core ones: a multiple of 8.
+bool diff_mma_supports(const Geometry &g);
+cudaError_t launch_diff_attend_mma(const DiffArgs &a, cudaStream_t stream);
+cudaError_t launch_diff_backward_mma(const DiffArgs &a, cudaStream_t stream);
+cudaError_t launch_diff_simt(const DiffArgs &a, bool backward, bool bf16, cudaStream_t stream);
+// list [B, R * topk] and start [B, R + 1]: for each region the regions that route to it, in order.
+cudaError_t launch_diff_invert(const DiffArgs &a, int32_t *list, int32_t *start, cudaStream_t stream);
+// Partial sums that the backward kernels leave for each head's dlam.
+long long diff_backward_parts(const Geometry &g, bool mma);
+
+// ---------------------------------------------------------------- rotary positions
+
+struct RopeArgs {
+    const void *q, *k;
+    void *q_out, *k_out;
+    const float *freqs;   // [n]
+    const int32_t *pos;   // [B, N, axes] or NULL: the raster grid from (y0, x0)
+    int64_t y0, x0;
+    int B, H, W, C, heads, hd, n, axes;
+    int tensors;          // 2, or 1 where k is NULL
+    float mscale;
+    bool interleaved, inverse;
+};
+cudaError_t launch_rope(const RopeArgs &a, bool bf16, int num_sms, cudaStream_t stream);
+
+// ---------------------------------------------------------------- norms around a block
+
+struct NormArgs {
+    const void *x, *h, *dy, *ds;
+    void *s, *y, *dx, *dh;
+    const float *gate, *post_w, *post_b, *pre_w, *pre_b;
+    float *dgate, *dpost_w, *dpost_b, *dpre_w, *dpre_b;
+    float *part;       // [units][5][C]
+    int rows, images;  // rows of one image; images is 1 unless each has a gate of its own
+    int C, nvec;       // 16-byte vectors of a row
+    int chunks, per, units;
+    bool gate_images, layer;
+    float alpha, eps, inv_c;
+};
+bool norm_supports(int C, bool bf16);
+// Splits the rows over CTAs: sets chunks, per and units.
+void norm_plan(NormArgs &a, bool backward, int num_sms);
+// The forward pass, or the backward pass with its column sums (two kernels).
+cudaError_t launch_norm_residual(const NormArgs &a, bool bf16, bool backward, cudaStream_t stream);
+
 }  // namespace bra

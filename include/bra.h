@@ -198,6 +198,79 @@ bra_status bra_attend_backward(const void *q, const void *k, const void *v, cons
                                float *dq, float *dk, float *dv, int B, int H, int W, int C, int heads, int n_win,
                                int topk, bra_dtype dtype, void *stream);
 
+/* Differential attention over the routed regions: the difference of two softmax maps with a learned
+   weight for each head. Head j's channels [j*hd, (j+1)*hd) of q and k hold two maps' queries and keys,
+   q1, k1 in the first hd/2 and q2, k2 in the last; v and out use all hd. For a query of region r, over
+   the tokens of regions idx[b, r, 0..topk-1],
+     out = (softmax(s q1 k1^T) - lambda[j] softmax(s q2 k2^T)) v,   s = (hd/2)^-1/2.
+   n_win = 1 with topk = 1 attends over the whole map. lambda: device fp32 [heads] (the learned weight
+   itself; how a model forms it is the caller's); other arguments, the treatment of idx and the empty
+   row (out = 0) as bra_attend. bf16 with hd a multiple of 16 runs on the tensor cores (P rounded to
+   bf16 for the product with v, everything else fp32), the rest on CUDA cores in fp32; neither
+   depends on bra_set_attend_kernel. BRA_ERR_UNSUPPORTED: hd % 8 != 0, hd > 128 (the limit on
+   a region's row segment, W / n_win * C, holds for routing only). */
+bra_status bra_diff_attend(const void *q, const void *k, const void *v, const int32_t *idx, const float *lambda, void *out,
+                           int B, int H, int W, int C, int heads, int n_win, int topk, bra_dtype dtype, void *stream);
+
+/* bra_route then bra_diff_attend on one stream (one region routes to itself: idx is cleared and no
+   routing kernel runs). The means are kept in `out` like bra_forward's. */
+bra_status bra_forward_diff(const void *q, const void *k, const void *v, int32_t *idx, const float *lambda, void *out,
+                            int B, int H, int W, int C, int heads, int n_win, int topk, bra_dtype dtype, void *stream);
+
+/* Backward of bra_diff_attend with the routing index held fixed: the gradients of sum(dout * out) by
+   q, k, v and lambda. dq, dk, dv: device [B, H, W, C] of dtype, written (regions that nothing routes to
+   get 0): each element is summed in fp32 inside one CTA and rounded once, so the gradients are the same
+   bits on every run and nothing wider would be gained; they must not overlap the inputs. dlambda: device
+   fp32 [heads], written (0 for B == 0). Takes scratch from the pool: 16 bytes for each (token, head), and
+   the index sorted by routed region. BRA_ERR_UNSUPPORTED: as bra_diff_attend, or
+   H * W * topk > 2^30. */
+bra_status bra_diff_attend_backward(const void *q, const void *k, const void *v, const int32_t *idx, const float *lambda,
+                                    const void *dout, void *dq, void *dk, void *dv, float *dlambda, int B, int H, int W,
+                                    int C, int heads, int n_win, int topk, bra_dtype dtype, void *stream);
+
+/* Rotary positions of q and k. The first 2 * axes * n channels of every head (hd = C / heads, even) are
+   `axes` blocks of n pairs, the rest is copied. Pair i of block a is turned by the angle
+   position[a] * freqs[i] and scaled by mscale; the pairs are channels (i, i + n) of the block, or
+   (2 i, 2 i + 1) where `interleaved` is not 0. axes = 2: the token's row and column, y0 + y and x0 + x;
+   axes = 1: its raster number (y0 + y) * W + x0 + x. positions, where not NULL, gives them instead: device
+   int32 [B, H, W, axes] (y0 and x0 are not used then). inverse turns by the negative angles and keeps
+   mscale: the gradients' way back. freqs: device fp32 [n]. k and k_out may both be NULL. An output may be
+   its own input (in place), and otherwise shares no memory with an input or the other output. Angles are
+   reduced in 64 bits, products are fp32, rounded to dtype. For differential attention each map's
+   half head is a head here. */
+bra_status bra_rope(const void *q, const void *k, void *q_out, void *k_out, const float *freqs, const int32_t *positions,
+                    int64_t y0, int64_t x0, int B, int H, int W, int C, int heads, int n, int axes, int interleaved,
+                    int inverse, float mscale, bra_dtype dtype, void *stream);
+
+typedef enum { BRA_NORM_LAYER = 0, BRA_NORM_RMS = 1 } bra_norm_kind;
+
+/* The norms around a block with its gate and residual scale, per token row of C channels:
+     s = alpha * x + gate * (norm(h) * post_weight + post_bias),   y = norm(s) * pre_weight + pre_bias,
+   x the residual stream, h the block's output, norm a LayerNorm (biased variance) or an RMS norm
+   with eps. post_weight NULL: h itself takes norm(h)'s place; h NULL: s = alpha * x, and s_out may be NULL;
+   pre_weight NULL: no y (y_out NULL); biases NULL: none; gate NULL: 1. x, h, s_out, y_out: device
+   [B, H, W, C] of dtype; weights, biases: device fp32 [C]; gate: device fp32 [gate_images, C] with
+   gate_images 1 or B (0 without a gate); all 16-byte aligned. s is rounded for s_out; y is of the s before
+   that rounding. s_out and y_out are distinct and may be x or h themselves. BRA_ERR_UNSUPPORTED:
+   C > 8192. */
+bra_status bra_norm_residual(const void *x, const void *h, const float *gate, int gate_images, const float *post_weight,
+                             const float *post_bias, const float *pre_weight, const float *pre_bias, float alpha, float eps,
+                             bra_norm_kind kind, void *s_out, void *y_out, int B, int H, int W, int C, bra_dtype dtype,
+                             void *stream);
+
+/* Backward of bra_norm_residual from its inputs: the gradients of sum(ds * s) + sum(dy * y). dy is given
+   exactly where pre_weight is; ds NULL counts as 0 (one of the two is given). dx and, where h is given,
+   dh: device [B, H, W, C] of dtype, written; distinct, and may be one of x, h, dy, ds themselves. The weights'
+   gradients (device fp32, of their weights' shapes; each given exactly where its weight is) are summed in a
+   fixed order, the same bits on every run; for B == 0 they are 0. Takes scratch from the pool: 20 C
+   bytes for each CTA of the launch. */
+bra_status bra_norm_residual_backward(const void *x, const void *h, const void *dy, const void *ds, const float *gate,
+                                      int gate_images, const float *post_weight, const float *post_bias,
+                                      const float *pre_weight, const float *pre_bias, float alpha, float eps,
+                                      bra_norm_kind kind, void *dx, void *dh, float *dgate, float *dpost_weight,
+                                      float *dpost_bias, float *dpre_weight, float *dpre_bias, int B, int H, int W, int C,
+                                      bra_dtype dtype, void *stream);
+
 /* bra_forward on HOST buffers: copies q, k, v (host, [B, H, W, C]) to device scratch from
    the library's pool, runs the forward pass on `stream`, copies idx and out back to the
    host buffers and synchronises `stream` before returning. Page-locked host memory gives
