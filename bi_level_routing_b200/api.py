@@ -313,39 +313,49 @@ def attend_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, idx: torc
     return dq, dk, dv
 
 
-def _on_device(device, fn, *args) -> int:
-    """fn(*args, stream) with `device` current and its current stream: the tensors' device need not be
-    the caller's."""
-    if torch.cuda.current_device() == device.index:
-        return fn(*args, _stream(device))
-    with torch.cuda.device(device):
-        return fn(*args, _stream(device))
+def _on_device(t: torch.Tensor, fn, *args) -> int:
+    """fn(*args, stream) with t's device current, on its current stream: the tensors' device need not be the
+    caller's current one."""
+    index = t.get_device()
+    if torch.cuda.current_device() == index:
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(index):
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
 
 
-def _routed(idx: torch.Tensor, q: torch.Tensor, n_win: int):
-    if (idx.dim() != 3 or idx.shape[:2] != (q.shape[0], n_win * n_win) or idx.dtype != torch.int32
-            or not idx.is_contiguous() or idx.device != q.device):
+def _alike(ref: torch.Tensor, what: str, *others):
+    """The checks of _same, for the (name, tensor) pairs whose tensor is not None."""
+    shape, dtype, device = ref.shape, ref.dtype, ref.get_device()
+    for name, t in others:
+        if t is None:
+            continue
+        if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+            raise ValueError(f"{name} must match {what} in shape, dtype and device")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _routed(idx: torch.Tensor, q: torch.Tensor, n_win: int) -> int:
+    """Checks a routing index for q and returns its topk."""
+    shape = idx.shape
+    if (len(shape) != 3 or shape[0] != q.shape[0] or shape[1] != n_win * n_win or idx.dtype is not torch.int32
+            or not idx.is_contiguous() or idx.get_device() != q.get_device()):
         raise ValueError("idx must be a contiguous int32 [B, n_win^2, topk] tensor on q's device")
+    return shape[2]
 
 
-def _vector(t: torch.Tensor | None, name: str, shapes, device):
-    """A contiguous fp32 tensor of one of `shapes` on `device`, or None."""
-    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) not in shapes or not t.is_contiguous()
-                          or t.device != device):
+def _vector(t: torch.Tensor | None, name: str, device: int, *shapes):
+    """The address of a contiguous fp32 tensor of one of `shapes` on `device`, or None for None."""
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.shape not in shapes or t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor of shape {' or '.join(map(str, shapes))} on "
-                         f"{device}")
-    return t
+                         "the maps' device")
+    return t.data_ptr()
 
 
 def _ptr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
-
-
-def _output(t: torch.Tensor | None, like: torch.Tensor, name: str) -> torch.Tensor:
-    if t is None:
-        return torch.empty_like(like)
-    _same(like, (name, t))
-    return t
 
 
 def diff_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, idx: torch.Tensor, lam: torch.Tensor, heads: int,
@@ -353,13 +363,13 @@ def diff_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, idx: torch.Te
     """Differential attention over the routed regions: per head the map of the first half of its q and k
     channels minus lam[head] times the map of the second half, times v. lam: float32 [heads]."""
     B, H, W, C = _shape(q, "q")
-    _same(q, ("k", k), ("v", v))
-    _routed(idx, q, n_win)
-    _vector(lam, "lam", [(heads,)], q.device)
-    out = _output(out, q, "out")
-    _check(_on_device(q.device, lib().bra_diff_attend, q.data_ptr(), k.data_ptr(), v.data_ptr(), idx.data_ptr(),
-                      lam.data_ptr(), out.data_ptr(), B, H, W, C, heads, n_win, idx.shape[-1], DTYPES[q.dtype]),
-           "bra_diff_attend")
+    _alike(q, "q", ("k", k), ("v", v), ("out", out))
+    topk = _routed(idx, q, n_win)
+    weight = _vector(lam, "lam", q.get_device(), (heads,))
+    if out is None:
+        out = torch.empty_like(q)
+    _check(_on_device(q, lib().bra_diff_attend, q.data_ptr(), k.data_ptr(), v.data_ptr(), idx.data_ptr(), weight,
+                      out.data_ptr(), B, H, W, C, heads, n_win, topk, DTYPES[q.dtype]), "bra_diff_attend")
     return out
 
 
@@ -367,17 +377,16 @@ def forward_diff(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.T
                  out: torch.Tensor | None = None, idx: torch.Tensor | None = None):
     """Routing, then differential attention. Returns (out, idx)."""
     B, H, W, C = _shape(q, "q")
-    _same(q, ("k", k), ("v", v))
-    _vector(lam, "lam", [(heads,)], q.device)
-    out = _output(out, q, "out")
+    _alike(q, "q", ("k", k), ("v", v), ("out", out))
+    weight = _vector(lam, "lam", q.get_device(), (heads,))
+    if out is None:
+        out = torch.empty_like(q)
     if idx is None:
         idx = torch.empty((B, n_win * n_win, topk), dtype=torch.int32, device=q.device)
-    _routed(idx, q, n_win)
-    if idx.shape[-1] != topk:
+    if _routed(idx, q, n_win) != topk:
         raise ValueError("idx must be a contiguous int32 [B, n_win^2, topk] tensor")
-    _check(_on_device(q.device, lib().bra_forward_diff, q.data_ptr(), k.data_ptr(), v.data_ptr(), idx.data_ptr(),
-                      lam.data_ptr(), out.data_ptr(), B, H, W, C, heads, n_win, topk, DTYPES[q.dtype]),
-           "bra_forward_diff")
+    _check(_on_device(q, lib().bra_forward_diff, q.data_ptr(), k.data_ptr(), v.data_ptr(), idx.data_ptr(), weight,
+                      out.data_ptr(), B, H, W, C, heads, n_win, topk, DTYPES[q.dtype]), "bra_forward_diff")
     return out, idx
 
 
@@ -388,14 +397,16 @@ def diff_attend_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, idx:
     """(dq, dk, dv, dlam): gradients of sum(dout * diff_attend(q, k, v, idx, lam)), idx fixed. dq, dk and dv
     have q's type, dlam is float32 [heads]; the same bits on every run."""
     B, H, W, C = _shape(q, "q")
-    _same(q, ("k", k), ("v", v), ("dout", dout))
-    _routed(idx, q, n_win)
-    _vector(lam, "lam", [(heads,)], q.device)
-    dq, dk, dv = _output(dq, q, "dq"), _output(dk, q, "dk"), _output(dv, q, "dv")
-    dlam = torch.empty_like(lam) if dlam is None else _vector(dlam, "dlam", [(heads,)], q.device)
-    _check(_on_device(q.device, lib().bra_diff_attend_backward, q.data_ptr(), k.data_ptr(), v.data_ptr(), idx.data_ptr(),
-                      lam.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dlam.data_ptr(), B, H,
-                      W, C, heads, n_win, idx.shape[-1], DTYPES[q.dtype]), "bra_diff_attend_backward")
+    _alike(q, "q", ("k", k), ("v", v), ("dout", dout), ("dq", dq), ("dk", dk), ("dv", dv))
+    topk = _routed(idx, q, n_win)
+    weight = _vector(lam, "lam", q.get_device(), (heads,))
+    dq, dk, dv = (torch.empty_like(q) if t is None else t for t in (dq, dk, dv))
+    if dlam is None:
+        dlam = torch.empty_like(lam)
+    _check(_on_device(q, lib().bra_diff_attend_backward, q.data_ptr(), k.data_ptr(), v.data_ptr(), idx.data_ptr(), weight,
+                      dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                      _vector(dlam, "dlam", q.get_device(), (heads,)), B, H, W, C, heads, n_win, topk, DTYPES[q.dtype]),
+           "bra_diff_attend_backward")
     return dq, dk, dv, dlam
 
 
@@ -408,22 +419,23 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, freqs: torch.Tensor, heads: in
     [B, H, W, axes]. inverse=True takes gradients back. q_out may be q, k_out k (in place).
     Returns (q_out, k_out). See rope_frequencies for freqs and mscale."""
     B, H, W, C = _shape(q, "q")
-    if k is not None:
-        _same(q, ("k", k))
-    elif k_out is not None:
+    if k is None and k_out is not None:
         raise ValueError("k_out without k")
-    _vector(freqs, "freqs", [(freqs.numel(),)], q.device)
-    if pos is not None and (tuple(pos.shape) != (B, H, W, axes) or pos.dtype != torch.int32 or not pos.is_contiguous()
-                            or pos.device != q.device):
+    _alike(q, "q", ("k", k), ("q_out", q_out), ("k_out", k_out))
+    n = freqs.numel()
+    table = _vector(freqs, "freqs", q.get_device(), (n,))
+    if pos is not None and (pos.shape != (B, H, W, axes) or pos.dtype is not torch.int32 or not pos.is_contiguous()
+                            or pos.get_device() != q.get_device()):
         raise ValueError("pos must be a contiguous int32 [B, H, W, axes] tensor on q's device")
     if layout not in ROPE_LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
-    q_out = _output(q_out, q, "q_out")
-    if k is not None:
-        k_out = _output(k_out, k, "k_out")
-    _check(_on_device(q.device, lib().bra_rope, q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), freqs.data_ptr(),
-                      _ptr(pos), int(origin[0]), int(origin[1]), B, H, W, C, heads, freqs.numel(), axes,
-                      ROPE_LAYOUTS[layout], int(inverse), float(mscale), DTYPES[q.dtype]), "bra_rope")
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    if k is not None and k_out is None:
+        k_out = torch.empty_like(k)
+    _check(_on_device(q, lib().bra_rope, q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), table, _ptr(pos),
+                      int(origin[0]), int(origin[1]), B, H, W, C, heads, n, axes, ROPE_LAYOUTS[layout], int(inverse),
+                      float(mscale), DTYPES[q.dtype]), "bra_rope")
     return q_out, k_out
 
 
@@ -460,17 +472,17 @@ def rope_frequencies(n: int, base: float = 10000.0, scaling: str = "none", facto
 
 
 def _norm_arguments(x, h, gate, post_weight, post_bias, pre_weight, pre_bias, alpha, eps, kind):
-    """Checks the arguments both norm calls share; returns (shape, gate_images, kind code)."""
+    """Checks the arguments both norm calls share; returns (shape, those from the gate to the kind for the C call)."""
     B, H, W, C = _shape(x, "x")
-    if h is not None:
-        _same(x, ("h", h))
-    for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("pre_weight", pre_weight),
-                    ("pre_bias", pre_bias)):
-        _vector(t, name, [(C,)], x.device)
-    _vector(gate, "gate", [(C,), (B, C)], x.device)
     if kind not in NORM_KINDS:
         raise ValueError(f"kind must be one of {sorted(NORM_KINDS)}, got {kind!r}")
-    return (B, H, W, C), (0 if gate is None else 1 if gate.dim() == 1 else B), NORM_KINDS[kind]
+    device, per_channel = x.get_device(), (C,)
+    gates = 0 if gate is None else 1 if gate.dim() == 1 else B
+    return (B, H, W, C), (_vector(gate, "gate", device, per_channel, (B, C)), gates,
+                          _vector(post_weight, "post_weight", device, per_channel),
+                          _vector(post_bias, "post_bias", device, per_channel),
+                          _vector(pre_weight, "pre_weight", device, per_channel),
+                          _vector(pre_bias, "pre_bias", device, per_channel), float(alpha), float(eps), NORM_KINDS[kind])
 
 
 def norm_residual(x: torch.Tensor, h: torch.Tensor | None = None, gate: torch.Tensor | None = None,
@@ -483,16 +495,16 @@ def norm_residual(x: torch.Tensor, h: torch.Tensor | None = None, gate: torch.Te
     post_weight h is taken as it is, without h s = alpha * x, without pre_weight there is no y. Weights, biases:
     float32 [C]; gate: float32 [C] or, one for each image, [B, C]. Returns (s, y); s is None where h is None
     (unless s_out is given), y where pre_weight is None."""
-    shape, gates, code = _norm_arguments(x, h, gate, post_weight, post_bias, pre_weight, pre_bias, alpha, eps, kind)
-    if h is not None or s_out is not None:
-        s_out = _output(s_out, x, "s_out")
-    if pre_weight is not None:
-        y_out = _output(y_out, x, "y_out")
-    elif y_out is not None:
+    shape, middle = _norm_arguments(x, h, gate, post_weight, post_bias, pre_weight, pre_bias, alpha, eps, kind)
+    _alike(x, "x", ("h", h), ("s_out", s_out), ("y_out", y_out))
+    if h is not None and s_out is None:
+        s_out = torch.empty_like(x)
+    if pre_weight is not None and y_out is None:
+        y_out = torch.empty_like(x)
+    elif pre_weight is None and y_out is not None:
         raise ValueError("y_out without pre_weight")
-    _check(_on_device(x.device, lib().bra_norm_residual, x.data_ptr(), _ptr(h), _ptr(gate), gates, _ptr(post_weight),
-                      _ptr(post_bias), _ptr(pre_weight), _ptr(pre_bias), float(alpha), float(eps), code, _ptr(s_out),
-                      _ptr(y_out), *shape, DTYPES[x.dtype]), "bra_norm_residual")
+    _check(_on_device(x, lib().bra_norm_residual, x.data_ptr(), _ptr(h), *middle, _ptr(s_out), _ptr(y_out), *shape,
+                      DTYPES[x.dtype]), "bra_norm_residual")
     return s_out, y_out
 
 
@@ -516,20 +528,18 @@ def norm_residual_backward(x: torch.Tensor, h: torch.Tensor | None, dy: torch.Te
     """Gradients of sum(ds * s) + sum(dy * y) of norm_residual with the same arguments. dy is given exactly where
     pre_weight is; ds may be None (no gradient of s). dx and dh have x's type, the others are float32 of their
     inputs' shapes; the same bits on every run."""
-    shape, gates, code = _norm_arguments(x, h, gate, post_weight, post_bias, pre_weight, pre_bias, alpha, eps, kind)
-    for name, t in (("dy", dy), ("ds", ds)):
-        if t is not None:
-            _same(x, (name, t))
-    dx = _output(dx, x, "dx")
-    if h is not None:
-        dh = _output(dh, x, "dh")
-    elif dh is not None:
+    shape, middle = _norm_arguments(x, h, gate, post_weight, post_bias, pre_weight, pre_bias, alpha, eps, kind)
+    _alike(x, "x", ("h", h), ("dy", dy), ("ds", ds), ("dx", dx), ("dh", dh))
+    if dx is None:
+        dx = torch.empty_like(x)
+    if h is not None and dh is None:
+        dh = torch.empty_like(x)
+    elif h is None and dh is not None:
         raise ValueError("dh without h")
     dgate, dpw, dpb, dnw, dnb = (None if t is None else torch.empty_like(t)
                                  for t in (gate, post_weight, post_bias, pre_weight, pre_bias))
-    _check(_on_device(x.device, lib().bra_norm_residual_backward, x.data_ptr(), _ptr(h), _ptr(dy), _ptr(ds), _ptr(gate),
-                      gates, _ptr(post_weight), _ptr(post_bias), _ptr(pre_weight), _ptr(pre_bias), float(alpha), float(eps),
-                      code, dx.data_ptr(), _ptr(dh), _ptr(dgate), _ptr(dpw), _ptr(dpb), _ptr(dnw), _ptr(dnb), *shape,
+    _check(_on_device(x, lib().bra_norm_residual_backward, x.data_ptr(), _ptr(h), _ptr(dy), _ptr(ds), *middle,
+                      dx.data_ptr(), _ptr(dh), _ptr(dgate), _ptr(dpw), _ptr(dpb), _ptr(dnw), _ptr(dnb), *shape,
                       DTYPES[x.dtype]), "bra_norm_residual_backward")
     return NormGrads(dx, dh, dgate, dpw, dpb, dnw, dnb)
 

@@ -569,11 +569,11 @@ namespace {
 
 size_t round16(size_t x) { return (x + 15) & ~(size_t)15; }
 
-template <typename K> cudaError_t launch_with(K kernel, int grid, size_t smem, const DiffArgs &a, cudaStream_t stream)
+template <auto Kernel> cudaError_t launch_with(int grid, size_t smem, const DiffArgs &a, cudaStream_t stream)
 {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = grant_shared_memory<Kernel>();
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3(grid), dim3(32 * kWarps), smem, stream, a);
+    return launch_pdl(Kernel, dim3(grid), dim3(32 * kWarps), smem, stream, a);
 }
 
 template <int DK, int WPI, int KT, int QT> cudaError_t launch_one(DiffArgs &a, cudaStream_t stream)
@@ -586,11 +586,11 @@ template <int DK, int WPI, int KT, int QT> cudaError_t launch_one(DiffArgs &a, c
     a.nitems = (int)items;
     a.nparts = (int)(items / a.heads * WPI);
     const int grid = (int)((items + groups - 1) / groups);
-    cudaError_t e = launch_with(diff_backward_queries_kernel<DK, WPI, KT>, grid,
+    cudaError_t e = launch_with<diff_backward_queries_kernel<DK, WPI, KT>>(grid,
                                 groups * ((size_t)4 * KT * ROW * 2 + round16((size_t)a.topk * 4) + 16), a, stream);
     if (e != cudaSuccess) return e;
     constexpr size_t tile = (size_t)4 * QT * ROW * 2, keep = (size_t)16 * WPI * ROW * 2;
-    return launch_with(diff_backward_keys_kernel<DK, WPI, QT>, grid > a.heads ? grid : a.heads,
+    return launch_with<diff_backward_keys_kernel<DK, WPI, QT>>(grid > a.heads ? grid : a.heads,
                        groups * ((tile > keep ? tile : keep) + 2 * QT * sizeof(float4)), a, stream);
 }
 

@@ -255,8 +255,7 @@ template <int DK, int WPI, int KT> cudaError_t launch_one(DiffArgs &a, cudaStrea
     if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     a.nitems = (int)items;
     const size_t smem = L::kGroups * L::group_bytes(a.topk);
-    cudaError_t e = cudaFuncSetAttribute(diff_attend_mma_kernel<DK, WPI, KT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = grant_shared_memory<diff_attend_mma_kernel<DK, WPI, KT>>();
     if (e != cudaSuccess) return e;
     const int grid = (int)((items + L::kGroups - 1) / L::kGroups);
     return launch_pdl(diff_attend_mma_kernel<DK, WPI, KT>, dim3(grid), dim3(32 * kWarps), smem, stream, a);

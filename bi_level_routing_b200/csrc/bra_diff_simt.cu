@@ -461,12 +461,12 @@ __global__ void __launch_bounds__(32 * WARPS) diff_backward_keys_simt_kernel(con
 
 namespace {
 
-template <typename K>
-cudaError_t launch_with(K kernel, int grid, int threads, size_t smem, const DiffArgs &a, cudaStream_t stream)
+template <auto Kernel>
+cudaError_t launch_with(int grid, int threads, size_t smem, const DiffArgs &a, cudaStream_t stream)
 {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = grant_shared_memory<Kernel>();
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3(grid), dim3(threads), smem, stream, a);
+    return launch_pdl(Kernel, dim3(grid), dim3(threads), smem, stream, a);
 }
 
 template <typename T, int WARPS, int RW, int NC> cudaError_t launch_one(DiffArgs &a, bool backward, cudaStream_t stream)
@@ -481,12 +481,12 @@ template <typename T, int WARPS, int RW, int NC> cudaError_t launch_one(DiffArgs
     const size_t tail = 16 + (((size_t)a.topk * 4 + 15) & ~(size_t)15);
     const int grid = (int)items;
     if (!backward)
-        return launch_with(diff_attend_simt_kernel<T, WARPS, RW, NC>, grid, 32 * WARPS, 4 * L::floats(a.hd, 1, 2) + tail, a,
+        return launch_with<diff_attend_simt_kernel<T, WARPS, RW, NC>>(grid, 32 * WARPS, 4 * L::floats(a.hd, 1, 2) + tail, a,
                            stream);
-    const cudaError_t e = launch_with(diff_backward_queries_simt_kernel<T, WARPS, RW, NC>, grid, 32 * WARPS,
+    const cudaError_t e = launch_with<diff_backward_queries_simt_kernel<T, WARPS, RW, NC>>(grid, 32 * WARPS,
                                       4 * L::floats(a.hd, 2, 2) + tail, a, stream);
     if (e != cudaSuccess) return e;
-    return launch_with(diff_backward_keys_simt_kernel<T, WARPS, RW, NC>, grid > a.heads ? grid : a.heads, 32 * WARPS,
+    return launch_with<diff_backward_keys_simt_kernel<T, WARPS, RW, NC>>(grid > a.heads ? grid : a.heads, 32 * WARPS,
                        4 * L::floats(a.hd, 2, 3), a, stream);
 }
 

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <string>
 #include <utility>
 
@@ -41,6 +42,21 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Lets Kernel, which holds no static shared memory, be launched with all the shared memory a block
+// may have (227 KB), once for each device: the call costs as much as a launch.
+template <auto Kernel> cudaError_t grant_shared_memory()
+{
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+    return e;
 }
 
 // Sets the message bra_last_error_message returns on this thread.
@@ -192,6 +208,9 @@ struct DiffArgs;  // bra_diff.cuh
 void diff_plan(DiffArgs &a, const Geometry &g);
 // The bf16 tensor-core kernels: hd a multiple of 16 up to 128. The CUDA-core ones: a multiple of 8.
 bool diff_mma_supports(const Geometry &g);
+// The tcgen05 ones (bf16): heads of 64 or 128 channels, large regions.
+bool diff_umma_supports(const Geometry &g);
+cudaError_t launch_diff_attend_umma(const DiffArgs &a, cudaStream_t stream);
 cudaError_t launch_diff_attend_mma(const DiffArgs &a, cudaStream_t stream);
 cudaError_t launch_diff_backward_mma(const DiffArgs &a, cudaStream_t stream);
 cudaError_t launch_diff_simt(const DiffArgs &a, bool backward, bool bf16, cudaStream_t stream);

