@@ -113,6 +113,12 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
 }
+// Arrives on `bar` once all cp.async copies this thread has issued have landed (the barrier's count
+// includes the thread).
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 template <int N> __device__ __forceinline__ void cp_async_wait_but()
 {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -124,6 +130,61 @@ __device__ __forceinline__ float finite_max(float before, float top)
 {
     const float m = fmaxf(before, top);
     return m == -INFINITY ? 0.f : m;
+}
+
+// 2^x of two values on the FMA pipe, for probabilities that are rounded to bf16: x = n + f with n the
+// nearest integer (added to 1.5 2^23, where a float's last bit counts ones), 2^f a cubic fitted to least
+// relative error on [-1/2, 1/2] (7.5e-5, a 26th of a bf16 rounding), n added to its exponent. x below
+// -126 counts as -126. NaN gives a finite value: callers' rows hold NaN in their maximum or other pairs.
+__device__ __forceinline__ float2 poly_exp2(float2 x)
+{
+    const float2 magic = make_float2(12582912.f, 12582912.f), back = make_float2(-12582912.f, -12582912.f);
+    x = make_float2(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f));
+    const float2 n = __fadd2_rn(x, magic);
+    const float2 m = __fadd2_rn(n, back);
+    const float2 f = __ffma2_rn(m, make_float2(-1.f, -1.f), x);
+    float2 p = __ffma2_rn(f, make_float2(0.05517120659351349f, 0.05517120659351349f),
+                          make_float2(0.24261026084423065f, 0.24261026084423065f));
+    p = __ffma2_rn(p, f, make_float2(0.6932609677314758f, 0.6932609677314758f));
+    p = __ffma2_rn(p, f, make_float2(0.9999281167984009f, 0.9999281167984009f));
+    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(n.x) << 23)),
+                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(n.y) << 23)));
+}
+
+// ---------------------------------------------------------------- tcgen05, issued by a converged warp
+//
+// A thread that issues products inside `if (lane == 0)` copies every descriptor from vector to uniform
+// registers first (60 cycles a product and 85 a commit were measured); in a converged warp the
+// compiler keeps them uniform, and one elected lane issues. uniform() tells it that a value is the same in
+// all lanes.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// Upper and lower half of a descriptor of 128-byte swizzled rows (umma_desc_sw128); x bytes further on is
+// + (x >> 4) of the lower half.
+constexpr uint32_t kDescHigh = (uint32_t)((1024 >> 4) | (1u << 14) | (2u << 29));
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr) { return ((saddr >> 4) & 0x3FFFu) | (1u << 16); }
+// D[tmem] (+)= A[smem] B[smem] and A[tmem] B[smem], bf16 into fp32
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a_low), "r"(b_low), "r"(idesc), "r"((uint32_t)add), "r"(kDescHigh)
+        : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_low, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b_low), "r"(idesc), "r"((uint32_t)add), "r"(kDescHigh)
+        : "memory");
 }
 
 __device__ __forceinline__ float quad_max(float x)

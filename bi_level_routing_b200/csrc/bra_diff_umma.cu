@@ -1,22 +1,25 @@
 // bra_diff_umma.cu -- forward differential attention of bf16 maps on the 5th-generation tensor cores
-// (tcgen05, TMEM accumulators), for heads of 64 or 128 channels and regions of at least
-// kUmmaRegion tokens (see bra_diff.cuh for the formula). Two exponentials a query-key pair against 6 hd
-// tensor operations: from these sizes on the exponential unit (16 a cycle and SM) is the bound.
+// (tcgen05, TMEM accumulators), for heads of 16 to 128 channels in multiples of 16 and large regions (see
+// bra_diff.cuh for the formula). Heads are padded with zeros to 64 or 128 channels. Two exponentials a query-key pair against 6 hd
+// tensor operations: the exponential unit (16 a cycle and SM) is the bound, 1024 cycles for 128 queries and 64
+// keys; 16384-token maps (2 images, 2 heads of 64) take 749 us, 1.25 times that at the clock they run at.
 //
-// A CTA owns 128 query tokens of one (image, region, head) and meets the routed keys in tiles of 128:
+// A CTA owns 128 query tokens of one (image, region, head) and meets the routed keys in tiles of KT: 32 for heads
+// of up to 64 channels, whose accumulators leave room in TMEM for two CTAs on an SM (four softmax warps a
+// scheduler; one CTA with tiles of 64 takes 776 us there, and 43 instead of 35 us on 256-token regions),
+// 64 for larger heads.
 //  * warps 0-3 are map 1's softmax, warps 4-7 map 2's; thread t of either owns query row t, i.e. TMEM
-//    lane t. While one map's scores are formed or its values summed, the other's exponentials run.
-//    A thread takes its row's 128 scores, follows the running maximum, writes the probabilities as bf16
-//    over the first 64 columns of its scores, and keeps the row's sum in fp32. The accumulator in
-//    TMEM is rescaled only when a row's maximum has grown by more than 2^8 (the probabilities stay
-//    relative to an older maximum until then: exact, and far from overflow), so PV products
-//    accumulate in place;
-//  * warp 8: one thread issues the products. S_m = Q_m K_m^T (M = N = 128, K = hd / 2) and
-//    O_m += P_m V (M = 128, N = 64 a block, K = 128; P from TMEM), map 1's and map 2's in turn: S_m of
-//    the next tile follows O_m of this one at once, since P_m lies over S_m;
-//  * warps 9-11 gather the query rows and, into a ring of stages, the key and value rows of the routed
-//    regions by cp.async, 128-byte swizzled; regions of any size pack densely, rows past the last key
-//    are zeros.
+//    lane t. It takes its row's scores, follows the running maximum, writes the probabilities as bf16
+//    over the first half of its scores, and keeps the row's sum in fp32. The accumulator in TMEM
+//    is rescaled only when a row's maximum has grown by more than 2^8 (the probabilities stay relative
+//    to an older maximum until then: exact, and far from overflow), so PV products accumulate in place;
+//  * warp 8: one elected lane issues the products. S_m = Q_m K_m^T (M = 128, N = KT, K = hd / 2) and
+//    O_m += P_m V (M = 128, N = 64 a block, K = KT; P from TMEM). Each map has two score buffers: the
+//    scores of the next tile are there when the softmax comes to them;
+//  * warps 9-10 gather the key and value rows of the routed regions into a ring of stages by cp.async,
+//    128-byte swizzled; regions of any size pack densely, rows past the last key are zeros. A lane finds
+//    the address of one row, eight lanes copy it. Warp 11 gathers the query rows and hands the
+//    tiles that have landed to warp 8.
 // Every wait is bounded (kErrTimeout); no thread leaves before the TMEM is released.
 #include "bra_diff.cuh"
 
@@ -24,47 +27,61 @@ namespace bra {
 
 namespace {
 
-constexpr int kThreads = 384, kLoaders = 96;
-constexpr int kBlock = 128 * 128;  // one tile of 128 rows x 64 channels
-constexpr uint32_t kCols = 512;    // S1 at 0, S2 at 128, O1 at 256, O2 after it
-// Registers a thread after the split; the launcher checks that the launch holds their sum.
-constexpr int kManyRegs = 200, kFewRegs = 80;
-constexpr float kGrowth = 8.f;     // log2 of the growth of a maximum that rescales the accumulator
+constexpr int kThreads = 384;
+// Pairs of exponentials out of 32 that go to the exponential unit; the others are polynomials on the FMA
+// pipe (16384-token map, 2 images of 2 heads of 64: all 32 778 us, 26 749 us, 20 767 us).
+constexpr int kUnitPairs = 26;
+constexpr int kQBlock = 128 * 128;       // 128 rows x 64 channels
+constexpr int kBarrierBytes = 512;       // room for the mbarriers
+constexpr float kGrowth = 8.f;           // log2 of the growth of a maximum that rescales the accumulator
 
-template <int NB> struct UmmaTile {
-    static constexpr int kStages = NB == 1 ? 4 : 3;
-    static size_t bytes(int topk) { return 1024 + (size_t)kBlock * NB * (1 + 2 * kStages) + 256 + 1024 + 16 + 4 * (size_t)topk; }
+// NB: 64-channel blocks of a head; KT: keys of a tile. TMEM: S of map m, buffer u at KT (2 m + u), O1 at
+// 4 KT, O2 after it.
+template <int NB, int KT> struct UmmaTile {
+    static constexpr int kStages = NB == 1 ? 8 : 5;
+    static constexpr int kBlock = KT * 128;
+    static constexpr uint32_t kCols = 4 * KT + 128 * NB <= 256 ? 256 : 512;  // an allocation is a power of two
+    static size_t bytes(int topk)
+    {
+        return 1024 + (size_t)NB * (kQBlock + 2 * kStages * kBlock) + kBarrierBytes + 1024 + 16 + 4 * (size_t)topk;
+    }
 };
 
 }  // namespace
 
-template <int NB> __global__ void __launch_bounds__(kThreads, 1) diff_attend_umma_kernel(const DiffArgs a)
+template <int NB, int KT>
+__global__ void __launch_bounds__(kThreads, KT == 32 ? 2 : 1) diff_attend_umma_kernel(const DiffArgs a)
 {
-    using L = UmmaTile<NB>;
+    using L = UmmaTile<NB, KT>;
     constexpr int ST = L::kStages, KS = 2 * NB;  // KS: 16-channel steps of a half head
+    constexpr int kBlock = L::kBlock, W = KT / 32;
+    constexpr uint32_t kCols = L::kCols;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *sQ = smem, *sKV = smem + kBlock * NB;  // [stage][K, V][NB]
+    uint8_t *sQ = smem, *sKV = smem + kQBlock * NB;  // [stage][K, V][NB]
     uint64_t *q_full = reinterpret_cast<uint64_t *>(sKV + (size_t)ST * 2 * NB * kBlock);
-    uint64_t *kv_full = q_full + 1, *kv_empty = kv_full + ST;
-    uint64_t *s_full = kv_empty + ST, *p_full = s_full + 2, *o_done = p_full + 2, *drain = o_done + 2;
-    float *sum = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(q_full) + 256);  // [2][128]
+    uint64_t *q_ready = q_full + 1, *kv_full = q_ready + 1, *kv_ready = kv_full + ST, *kv_empty = kv_ready + ST;
+    uint64_t *s_full = kv_empty + ST;  // [map][buffer]
+    uint64_t *p_full = s_full + 4;     // [map][buffer]
+    uint64_t *drain = p_full + 4;
+    float *sum = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(q_full) + kBarrierBytes);  // [2][128]
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sum + 256);
     int *count = reinterpret_cast<int *>(tmem_slot + 1);
     int *bases = count + 3;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const DiffItem it = diff_item(a, blockIdx.x);
 
     if (threadIdx.x == 0) {
-        mbar_init(q_full, kLoaders / 32);
+        mbar_init(q_full, 32);
+        mbar_init(q_ready, 1);
         for (int i = 0; i < ST; ++i) {
-            mbar_init(&kv_full[i], kLoaders / 32);
+            mbar_init(&kv_full[i], KT);
+            mbar_init(&kv_ready[i], 1);
             mbar_init(&kv_empty[i], 1);
         }
-        for (int m = 0; m < 2; ++m) {
-            mbar_init(&s_full[m], 1);
-            mbar_init(&p_full[m], 4);
-            mbar_init(&o_done[m], 1);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
         }
         mbar_init(drain, 1);
         mbar_fence_init();
@@ -83,143 +100,196 @@ template <int NB> __global__ void __launch_bounds__(kThreads, 1) diff_attend_umm
     tcgen05_after_sync();
     const uint32_t tmem = *tmem_slot;
     const int nkeys = *count * a.rs;
-    const int ntiles = (nkeys + 127) / 128;
+    const int ntiles = (nkeys + KT - 1) / KT;
     const int64_t image = (int64_t)it.b * a.N * a.C + it.h * a.hd;
     const int region = region_at(a, it.r);
     const int tok0 = it.t * 128;
 
-    // the softmax warps' registers come from the others' (warps 8-11 are one warpgroup)
-    if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
     if (warp >= 9) {
         // ------------------------------------------------------------- gather
-        const int tid = threadIdx.x - 288, j = tid & 7;
-        const __nv_bfloat16 *gq = static_cast<const __nv_bfloat16 *>(a.q) + image + 8 * j;
-        const __nv_bfloat16 *gk = static_cast<const __nv_bfloat16 *>(a.k) + image + 8 * j;
-        const __nv_bfloat16 *gv = static_cast<const __nv_bfloat16 *>(a.v) + image + 8 * j;
-        if (ntiles > 0) {
-            for (int row = tid >> 3; row < 128; row += kLoaders / 8) {
-                const bool real = tok0 + row < a.rs;
-                const int64_t off = real ? (int64_t)token_at(a, region, tok0 + row) * a.C : 0;
+        const int j = lane & 7, sub = lane >> 3;  // this lane's 16-byte chunk (of each block) of rows 4 x + sub
+        // where that chunk comes from: halves of d channels padded with zeros to 32 NB for q and k, hd
+        // channels padded to 64 NB for v
+        const int dc = a.d / 8;
+        int c_half[NB];
+        bool in_half[NB], in_v[NB];
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-                    cp_async16_or_zero(smem_u32(sQ + nb * kBlock) + sw128(row, j), gq + off + 64 * nb, real);
-            }
-            cp_async_commit();
+        for (int nb = 0; nb < NB; ++nb) {
+            const int c = j + 8 * nb, m = c / (4 * NB), x = c % (4 * NB);
+            in_half[nb] = x < dc;
+            c_half[nb] = in_half[nb] ? 8 * (m * dc + x) : 0;
+            in_v[nb] = c < 2 * dc;
         }
-        // tile i's copies are committed, then tile i - LAG's have landed and are handed over; the queries
-        // came before tile 0. LAG = ST - 2: the products release a stage only after they have the
-        // next tile, so two tiles must be in hand before the ring's first stage is waited for.
-        constexpr int LAG = ST - 2;
-        bool alive = true;
-        for (int i = 0; i < ntiles + LAG && alive && ntiles > 0; ++i) {
-            if (i < ntiles) {
-                const int st = i % ST;
-                if (!(alive = mbar_wait(&kv_empty[st], (uint32_t)(((i / ST) & 1) ^ 1), a.err))) break;
-                uint8_t *sk = sKV + (size_t)st * 2 * NB * kBlock, *sv = sk + NB * kBlock;
-                for (int row = tid >> 3; row < 128; row += kLoaders / 8) {
-                    const int key = i * 128 + row;
-                    const bool real = key < nkeys;
-                    int64_t off = 0;
-                    if (real) {
-                        int slot, tok;
-                        a.by_rs.divmod(key, slot, tok);
-                        off = (int64_t)token_at(a, bases[slot], tok) * a.C;
-                    }
+        if (warp == 11) {
+            const __nv_bfloat16 *gq = static_cast<const __nv_bfloat16 *>(a.q) + image;
+            for (int r0 = 0; r0 < 128; r0 += 32) {
+                const int at = tok0 + r0 + lane < a.rs ? token_at(a, region, tok0 + r0 + lane) : -1;
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) {
-                        cp_async16_or_zero(smem_u32(sk + nb * kBlock) + sw128(row, j), gk + off + 64 * nb, real);
-                        cp_async16_or_zero(smem_u32(sv + nb * kBlock) + sw128(row, j), gv + off + 64 * nb, real);
-                    }
+                for (int x = 0; x < 8; ++x) {
+                    const int row = r0 + 4 * x + sub, tok = __shfl_sync(0xffffffffu, at, 4 * x + sub);
+                    const __nv_bfloat16 *src = gq + (int64_t)max(tok, 0) * a.C;
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+                        cp_async16_or_zero(smem_u32(sQ + nb * kQBlock) + sw128(row, j), src + c_half[nb], tok >= 0 && in_half[nb]);
                 }
             }
-            cp_async_commit();
-            cp_async_wait_but<LAG>();
+            cp_async_arrive(q_full);
+            // The copies are generic writes: between their landing and the products' reads stands a proxy
+            // fence. Here it holds up nothing but this warp (on the copying side it waits for
+            // every copy in flight, on the issuing side it takes 200 cycles a tile).
+            bool alive = ntiles > 0 && mbar_wait(q_full, 0, a.err);
             fence_async_shared();
-            __syncwarp();
-            if (lane == 0) {
-                if (i == LAG) mbar_arrive(q_full);
-                if (i >= LAG) mbar_arrive(&kv_full[(i - LAG) % ST]);
+            if (lane == 0 && alive) mbar_arrive(q_ready);
+            for (int i = 0; i < ntiles && alive; ++i) {
+                alive = mbar_wait(&kv_full[i % ST], (uint32_t)((i / ST) & 1), a.err);
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0 && alive) mbar_arrive(&kv_ready[i % ST]);
+            }
+        } else {
+            // 32 rows to a warp: the halves of a tile of 64, every other tile of 32
+            const __nv_bfloat16 *gk = static_cast<const __nv_bfloat16 *>(a.k) + image;
+            const __nv_bfloat16 *gv = static_cast<const __nv_bfloat16 *>(a.v) + image;
+            const int r0 = KT == 64 ? 32 * (warp - 9) : 0;
+            for (int i = KT == 64 ? 0 : warp - 9; i < ntiles; i += KT == 64 ? 1 : 2) {
+                const int st = i % ST, key = i * KT + r0 + lane;
+                int at = -1;
+                if (key < nkeys) {
+                    int slot, tok;
+                    a.by_rs.divmod(key, slot, tok);
+                    at = token_at(a, bases[slot], tok);
+                }
+                if (!mbar_wait(&kv_empty[st], (uint32_t)(((i / ST) & 1) ^ 1), a.err)) break;
+                const uint32_t sk = smem_u32(sKV + (size_t)st * 2 * NB * kBlock);
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const int tok = __shfl_sync(0xffffffffu, at, 4 * x + sub);
+                    const int64_t off = (int64_t)max(tok, 0) * a.C;
+                    const uint32_t dst = sk + sw128(r0 + 4 * x + sub, j);
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        cp_async16_or_zero(dst + nb * kBlock, gk + off + c_half[nb], tok >= 0 && in_half[nb]);
+                        cp_async16_or_zero(dst + (NB + nb) * kBlock, gv + off + (in_v[nb] ? 8 * j + 64 * nb : 0),
+                                           tok >= 0 && in_v[nb]);
+                    }
+                }
+                cp_async_arrive(&kv_full[st]);
             }
         }
         cp_async_wait_all();
-    } else {
+    } else if (warp == 8) {
         // ------------------------------------------------------------- products
-        if (lane == 0 && ntiles > 0) {
-            constexpr uint32_t kIdescS = umma_idesc_bf16(128, 128, false);
-            constexpr uint32_t kIdescPV = umma_idesc_bf16(128, 64, true);
-            const uint64_t dq = umma_desc_sw128(smem_u32(sQ)), dkv = umma_desc_sw128(smem_u32(sKV));
-            bool alive = mbar_wait(q_full, 0, a.err);
-            auto scores = [&](int m, int i) {  // half m's channels: 64 bytes on in the same rows, or the next block
-                const uint64_t half = NB == 1 ? 4 * m : (uint64_t)m * (kBlock >> 4);
-                const uint64_t dk = dkv + (uint64_t)((i % ST) * 2 * NB) * (kBlock >> 4) + half;
+        constexpr uint32_t kIdescS = umma_idesc_bf16(128, KT, false);
+        constexpr uint32_t kIdescPV = umma_idesc_bf16(128, 64, true);
+        const int nt = uniform(ntiles);
+        const uint32_t tm = uniform(tmem), dq = uniform(desc_low(smem_u32(sQ))), dkv = uniform(desc_low(smem_u32(sKV)));
+        const bool leader = elect_one();
+        bool alive = nt > 0 && mbar_wait(q_ready, 0, a.err);
+        int st = 0, next = 0;  // stages of tile i and of the next tile to form scores of
+        uint32_t phase = 0;
+        auto scores = [&](int m, uint32_t buf) {  // half m's channels: 64 bytes on in the same rows, or the next block
+            const uint32_t hq = NB == 1 ? 4 * m : m * (kQBlock >> 4), hk = NB == 1 ? 4 * m : m * (kBlock >> 4);
+            const uint32_t dk = dkv + next * (2 * NB * (kBlock >> 4)) + hk;
+            if (leader) {
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
-                    umma_bf16(tmem + 128 * m, dq + half + 2 * ks, dk + 2 * ks, kIdescS, (uint32_t)(ks > 0));
-                umma_commit(&s_full[m]);
-            };
-            if (alive) alive = mbar_wait(&kv_full[0], 0, a.err);
-            if (alive) {
-                tcgen05_after_sync();
-                scores(0, 0);
-                scores(1, 0);
+                    umma_ss(tm + KT * (2 * m + buf), dq + hq + 2 * ks, dk + 2 * ks, kIdescS, ks > 0);
             }
-            for (int i = 0; i < ntiles && alive; ++i) {
-                for (int m = 0; m < 2 && alive; ++m) {
-                    if (!(alive = mbar_wait(&p_full[m], (uint32_t)(i & 1), a.err))) break;
-                    tcgen05_after_sync();
-                    const uint64_t dv = dkv + (uint64_t)((i % ST) * 2 * NB + NB) * (kBlock >> 4);
+        };
+        auto advance = [&] {
+            if (++next == ST) {
+                next = 0;
+                phase ^= 1;
+            }
+        };
+        for (int i = 0; i < 2 && i < nt && alive; ++i) {
+            if (!(alive = mbar_wait(&kv_ready[next], phase, a.err))) break;
+            tcgen05_after_sync();
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                scores(m, i);
+                if (leader) umma_commit(&s_full[2 * m + i]);
+            }
+            __syncwarp();
+            advance();
+        }
+        for (int i = 0; i < nt && alive; ++i) {
+            const uint32_t buf = i & 1;
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                if (m == 0 && i + 2 < nt) alive = alive && mbar_wait(&kv_ready[next], phase, a.err);
+                alive = alive && mbar_wait(&p_full[2 * m + buf], (uint32_t)((i >> 1) & 1), a.err);
+                if (!alive) break;
+                tcgen05_after_sync();
+                const uint32_t dv = dkv + (st * 2 * NB + NB) * (kBlock >> 4);
+                if (leader) {
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            umma_bf16_ts(tmem + 256 + 64 * (NB * m + nb), tmem + 128 * m + 8 * ks,
-                                         dv + (uint64_t)nb * (kBlock >> 4) + 128 * ks, kIdescPV, (uint32_t)(i > 0 || ks > 0));
-                    umma_commit(&o_done[m]);
-                    if (m == 1) umma_commit(&kv_empty[i % ST]);
-                    if (i + 1 < ntiles) {
-                        if (m == 0) {
-                            if (!(alive = mbar_wait(&kv_full[(i + 1) % ST], (uint32_t)(((i + 1) / ST) & 1), a.err))) break;
-                            tcgen05_after_sync();
-                        }
-                        scores(m, i + 1);
-                    }
+                        for (int ks = 0; ks < KT / 16; ++ks)
+                            umma_ts(tm + 4 * KT + 64 * (NB * m + nb), tm + KT * (2 * m + buf) + 8 * ks,
+                                    dv + nb * (kBlock >> 4) + 128 * ks, kIdescPV, i > 0 || ks > 0);
                 }
+                // the tile after next takes the buffer whose probabilities were just read (products of one
+                // thread run in the order of their issue); the commit says that O_m holds tile i, too
+                if (i + 2 < nt) scores(m, buf);
+                if (leader) {
+                    umma_commit(&s_full[2 * m + buf]);
+                    if (m == 1) umma_commit(&kv_empty[st]);
+                }
+                __syncwarp();
             }
-            // wait for the last commit, so that no arrival lands after this CTA has left
-            umma_commit(drain);
-            mbar_wait(drain, 0, a.err);
+            if (i + 2 < nt) advance();
+            if (++st == ST) st = 0;
         }
-    }
+        // wait for the last commit, so that no arrival lands after this CTA has left
+        if (leader) umma_commit(drain);
+        __syncwarp();
+        mbar_wait(drain, 0, a.err);
     } else {
         // ------------------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
         const int m = warp >> 2, row = 32 * (warp & 3) + lane;
-        const uint32_t t_row = tmem + ((uint32_t)(32 * (warp & 3)) << 16), t_s = t_row + 128 * m;
-        const uint32_t t_o = t_row + 256 + 64 * NB * m;
+        const uint32_t t_row = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t t_o = t_row + 4 * KT + 64 * NB * m;
         float mx = -INFINITY, l = 0.f;
         bool alive = true;
         const float2 sc = make_float2(a.scale_log2, a.scale_log2);
         for (int i = 0; i < ntiles; ++i) {
-            if (!(alive = mbar_wait(&s_full[m], (uint32_t)(i & 1), a.err))) break;
+            const uint32_t t_s = t_row + KT * (2 * m + (i & 1));
+            if (!(alive = mbar_wait(&s_full[2 * m + (i & 1)], (uint32_t)((i >> 1) & 1), a.err))) break;
             tcgen05_after_sync();
-            uint32_t v[4][32];
+            // The exponentials are taken relative to the maximum so far while this tile's own is still
+            // being found; only where it has grown past kGrowth are they taken again.
+            uint32_t pw[KT / 2];
+            float t;
+            float2 ls[2];
+            auto probabilities = [&](float base) {
+                uint32_t v[W][32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld_32x32(t_s + 32 * c, v[c]);
-            tmem_wait_ld();
-            if ((i + 1) * 128 > nkeys) {
+                for (int c = 0; c < W; ++c) tmem_ld_32x32(t_s + 32 * c, v[c]);
+                tmem_wait_ld();
+                if ((i + 1) * KT > nkeys) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < W; ++c)
 #pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        if (i * 128 + 32 * c + x >= nkeys) v[c][x] = 0xff800000u;
-            }
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        for (int x = 0; x < 32; ++x)
+                            if (i * KT + 32 * c + x >= nkeys) v[c][x] = 0xff800000u;
+                }
+                const float2 nm = make_float2(base, base);
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                ls[0] = ls[1] = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int x = 0; x < 32; x += 2)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) top[c] = fmax3(top[c], __uint_as_float(v[c][x]), __uint_as_float(v[c][x + 1]));
-            const float t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+                for (int x = 0; x < KT / 2; ++x) {
+                    const float s0 = __uint_as_float(v[x / 16][(2 * x) % 32]), s1 = __uint_as_float(v[x / 16][(2 * x) % 32 + 1]);
+                    const float2 e = __ffma2_rn(make_float2(s0, s1), sc, nm);
+                    const float2 p = x * kUnitPairs % 32 < kUnitPairs ? make_float2(fast_exp2(e.x), fast_exp2(e.y)) : poly_exp2(e);
+                    top[x & 3] = fmax3(top[x & 3], s0, s1);
+                    ls[x & 1] = __fadd2_rn(ls[x & 1], p);
+                    pw[x] = pack_bf16x2(p.x, p.y);
+                }
+                t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+            };
+            probabilities(mx == -INFINITY ? 0.f : -mx);
             const bool grown = t > mx + kGrowth || (mx == -INFINITY && t != -INFINITY);
             if (__any_sync(0xffffffffu, grown)) {
                 const float corr = grown ? fast_exp2(mx - t) : 1.f;
@@ -227,8 +297,8 @@ template <int NB> __global__ void __launch_bounds__(kThreads, 1) diff_attend_umm
                     mx = t;
                     l *= corr;
                 }
-                if (i > 0) {  // the products so far are complete before they are rescaled
-                    if (!(alive = mbar_wait(&o_done[m], (uint32_t)((i - 1) & 1), a.err))) break;
+                if (i > 0) {  // O_m holds the tiles before this one once the next one's scores are there
+                    if (!(alive = mbar_wait(&s_full[2 * m + ((i + 1) & 1)], (uint32_t)(((i + 1) >> 1) & 1), a.err))) break;
                     tcgen05_after_sync();
 #pragma unroll
                     for (int c = 0; c < 2 * NB; ++c) {
@@ -241,35 +311,24 @@ template <int NB> __global__ void __launch_bounds__(kThreads, 1) diff_attend_umm
                     }
                     tmem_wait_st();
                 }
+                probabilities(mx == -INFINITY ? 0.f : -mx);
             }
-            const float base = mx == -INFINITY ? 0.f : -mx;
-            const float2 nm = make_float2(base, base);
-            float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t pw[32];
-#pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    const uint32_t s0 = v[2 * half + x / 16][(2 * x) % 32], s1 = v[2 * half + x / 16][(2 * x) % 32 + 1];
-                    const float2 e = __ffma2_rn(make_float2(__uint_as_float(s0), __uint_as_float(s1)), sc, nm);
-                    const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
-                    ls[x & 1] = __fadd2_rn(ls[x & 1], p);
-                    pw[x] = pack_bf16x2(p.x, p.y);
-                }
-                tmem_st_32x32(t_s + 32 * half, pw);
-            }
+            if constexpr (KT == 64)
+                tmem_st_32x32(t_s, pw);
+            else
+                tmem_st_32x16(t_s, pw);
             tmem_wait_st();
             const float2 add = __fadd2_rn(ls[0], ls[1]);
             l += add.x + add.y;
             tcgen05_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[m]);
+            if (lane == 0) mbar_arrive(&p_full[2 * m + (i & 1)]);
         }
         // out = O1 / l1 - lam O2 / l2: thread `row` of map m's warps writes half m of the row's channels
         sum[128 * m + row] = l;
         named_barrier(1, 256);
-        if (ntiles > 0 && alive) alive = mbar_wait(&o_done[0], (uint32_t)((ntiles - 1) & 1), a.err);
-        if (ntiles > 0 && alive) alive = mbar_wait(&o_done[1], (uint32_t)((ntiles - 1) & 1), a.err);
+        for (int x = 0; x < 2 && ntiles > 0 && alive; ++x)  // the commit after the last tile's products
+            alive = mbar_wait(&s_full[2 * x + ((ntiles + 1) & 1)], (uint32_t)(((ntiles + 1) >> 1) & 1), a.err);
         tcgen05_after_sync();
         const float l1 = sum[row], l2 = sum[128 + row], lam = __ldg(a.lam + it.h);
         const float w1 = l1 > 0.f ? 1.f / l1 : 0.f, w2 = l2 > 0.f ? -lam / l2 : 0.f;
@@ -280,8 +339,8 @@ template <int NB> __global__ void __launch_bounds__(kThreads, 1) diff_attend_umm
         for (int c = 0; c < NB; ++c) {
             uint32_t o1[32], o2[32];
             if (ntiles > 0) {  // the same for the whole CTA: tcgen05.ld is warp-wide
-                tmem_ld_32x32(t_row + 256 + 32 * NB * m + 32 * c, o1);
-                tmem_ld_32x32(t_row + 256 + 64 * NB + 32 * NB * m + 32 * c, o2);
+                tmem_ld_32x32(t_row + 4 * KT + 32 * NB * m + 32 * c, o1);
+                tmem_ld_32x32(t_row + 4 * KT + 64 * NB + 32 * NB * m + 32 * c, o2);
                 tmem_wait_ld();
             }
             if (!in || !alive) continue;
@@ -295,7 +354,7 @@ template <int NB> __global__ void __launch_bounds__(kThreads, 1) diff_attend_umm
                     const float w = fmaf(__uint_as_float(o1[z + 1]), w1, __uint_as_float(o2[z + 1]) * w2);
                     pk[y] = ntiles > 0 ? pack_bf16x2(u, w) : 0u;
                 }
-                *reinterpret_cast<uint4 *>(out + 32 * c + x) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                if (32 * NB * m + 32 * c + x < a.hd) *reinterpret_cast<uint4 *>(out + 32 * c + x) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             }
         }
     }
@@ -305,30 +364,22 @@ template <int NB> __global__ void __launch_bounds__(kThreads, 1) diff_attend_umm
     if (warp == 8) tmem_dealloc(tmem, kCols);
 }
 
-// From this many tokens a region's query tiles of 128 rows are full enough, and its keys many enough, that
-// the tensor-core pipeline beats the register-tiled kernel.
-constexpr int kUmmaRegion = 128;
-
-// Heads of 64 or 128 channels; with 128 the ring leaves room for rows of at most 188 routed regions.
+// Any head the register-tiled kernel takes; regions whose query tiles are more than half full, or just
+// half with many keys. Both kernels, heads of 64: 4 regions of 64 tokens to a query 36.5 against 41.4 us (16
+// images of 16 regions, 4 heads), of 100 tokens 50.8 against 112, of 144 117 against 215; but one
+// region of 64 tokens (64 images of 49 regions) 64 against 48.
 bool diff_umma_supports(const Geometry &g)
 {
-    if (g.rs < kUmmaRegion) return false;
-    return (g.hd == 64 && UmmaTile<1>::bytes(g.topk) <= 227 * 1024) || (g.hd == 128 && UmmaTile<2>::bytes(g.topk) <= 227 * 1024);
+    return diff_mma_supports(g) && (g.rs > 64 || (g.rs == 64 && g.topk >= 4));
 }
 
 namespace {
 
-template <int NB> cudaError_t launch_nb(const DiffArgs &a, int grid, cudaStream_t stream)
+template <int NB, int KT> cudaError_t launch_nb(const DiffArgs &a, int grid, cudaStream_t stream)
 {
-    cudaError_t e = grant_shared_memory<diff_attend_umma_kernel<NB>>();
+    const cudaError_t e = grant_shared_memory<diff_attend_umma_kernel<NB, KT>>();
     if (e != cudaSuccess) return e;
-    // registers of the launch, as compiled: a split that asks for more would wait forever
-    static const int regs = [] {
-        cudaFuncAttributes at;
-        return cudaFuncGetAttributes(&at, diff_attend_umma_kernel<NB>) == cudaSuccess ? at.numRegs : 0;
-    }();
-    if (regs * kThreads < 256 * kManyRegs + 128 * kFewRegs) return cudaErrorInvalidConfiguration;
-    return launch_pdl(diff_attend_umma_kernel<NB>, dim3(grid), dim3(kThreads), UmmaTile<NB>::bytes(a.topk), stream, a);
+    return launch_pdl(diff_attend_umma_kernel<NB, KT>, dim3(grid), dim3(kThreads), UmmaTile<NB, KT>::bytes(a.topk), stream, a);
 }
 
 }  // namespace
@@ -341,7 +392,7 @@ cudaError_t launch_diff_attend_umma(const DiffArgs &args, cudaStream_t stream)
     const long long items = (long long)a.B * a.R * a.tiles * a.heads;
     if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     a.nitems = (int)items;
-    return a.hd == 64 ? launch_nb<1>(a, (int)items, stream) : launch_nb<2>(a, (int)items, stream);
+    return a.hd <= 64 ? launch_nb<1, 32>(a, (int)items, stream) : launch_nb<2, 64>(a, (int)items, stream);
 }
 
 }  // namespace bra

@@ -208,7 +208,7 @@ struct DiffArgs;  // bra_diff.cuh
 void diff_plan(DiffArgs &a, const Geometry &g);
 // The bf16 tensor-core kernels: hd a multiple of 16 up to 128. The CUDA-core ones: a multiple of 8.
 bool diff_mma_supports(const Geometry &g);
-// The tcgen05 ones (bf16): heads of 64 or 128 channels, large regions.
+// The tcgen05 ones (bf16, the same heads): large regions.
 bool diff_umma_supports(const Geometry &g);
 cudaError_t launch_diff_attend_umma(const DiffArgs &a, cudaStream_t stream);
 cudaError_t launch_diff_attend_mma(const DiffArgs &a, cudaStream_t stream);

@@ -45,7 +45,7 @@ SHAPES = [
     (2, 8, 4, 2, 2, 1, 128), (1, 3, 11, 2, 4, 2, 64), (2, 8, 8, 3, 1, 1, 64), (1, 9, 7, 2, 3, 2, 80), (1, 10, 10, 2, 2, 1, 96),
     (1, 13, 10, 1, 1, 2, 64), (1, 1, 257, 1, 1, 1, 64), (1, 16, 17, 1, 1, 1, 128), (1, 8, 8, 2, 4, 1, 112), (1, 6, 6, 2, 3, 2, 16),
     (1, 16, 16, 1, 1, 1, 32), (1, 12, 11, 2, 3, 2, 64), (2, 16, 8, 2, 4, 1, 128), (1, 15, 9, 3, 5, 1, 64), (1, 1, 128, 1, 1, 2, 128),
-    (1, 20, 13, 2, 3, 1, 128), (1, 129, 1, 2, 2, 2, 64), (1, 1, 3, 16, 7, 1, 32), (2, 1, 2, 32, 5, 1, 16),
+    (1, 20, 13, 2, 3, 1, 128), (1, 8, 8, 3, 5, 2, 64), (1, 9, 9, 2, 2, 2, 16), (1, 11, 12, 2, 3, 1, 48), (1, 10, 7, 3, 4, 1, 112), (2, 8, 9, 2, 4, 1, 32), (1, 129, 1, 2, 2, 2, 64), (1, 1, 3, 16, 7, 1, 32), (2, 1, 2, 32, 5, 1, 16),
 ]
 ODD_HEADS = [(1, 3, 3, 2, 3, 2, 8), (1, 5, 2, 2, 2, 1, 24), (1, 1, 1, 3, 9, 2, 40), (1, 9, 8, 1, 1, 1, 56), (1, 4, 4, 2, 2, 1, 120)]
 
