@@ -714,7 +714,8 @@ static bra_status diff_attend_impl(const void *q, const void *k, const void *v, 
     a.out = out;
     a.err = st->error_word;
     const bool bf16 = dtype == BRA_BF16;
-    const cudaError_t e = bf16 && bra::diff_umma_supports(g)  ? bra::launch_diff_attend_umma(a, stream)
+    const cudaError_t e = bf16 && bra::diff_tile_supports(g)  ? bra::launch_diff_attend_tile(a, stream)
+                          : bf16 && bra::diff_umma_supports(g) ? bra::launch_diff_attend_umma(a, stream)
                           : bf16 && bra::diff_mma_supports(g) ? bra::launch_diff_attend_mma(a, stream)
                                                               : bra::launch_diff_simt(a, false, bf16, stream);
     return e == cudaSuccess ? BRA_OK : cuda_fail(e, "differential attention kernel");

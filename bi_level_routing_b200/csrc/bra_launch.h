@@ -208,6 +208,9 @@ struct DiffArgs;  // bra_diff.cuh
 void diff_plan(DiffArgs &a, const Geometry &g);
 // The bf16 tensor-core kernels: hd a multiple of 16 up to 128. The CUDA-core ones: a multiple of 8.
 bool diff_mma_supports(const Geometry &g);
+// The forward kernel for at most 64 keys a query (bf16, the same heads).
+bool diff_tile_supports(const Geometry &g);
+cudaError_t launch_diff_attend_tile(const DiffArgs &a, cudaStream_t stream);
 // The tcgen05 ones (bf16, the same heads): large regions.
 bool diff_umma_supports(const Geometry &g);
 cudaError_t launch_diff_attend_umma(const DiffArgs &a, cudaStream_t stream);

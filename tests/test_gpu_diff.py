@@ -115,6 +115,28 @@ def test_not_finite_outside_the_routed_regions(dtype, rs):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_not_finite_values_reach_their_own_queries(dtype):
+    """One infinite value: the queries whose rows name its region get an infinity or NaN in that channel,
+    all others and all other channels what they had."""
+    for hr, wr, n_win, hd in ((1, 1, 7, 64), (2, 3, 3, 32), (4, 4, 3, 64), (9, 9, 2, 64)):
+        q, k, v, idx, lam, _ = make(2, hr, wr, n_win, 2, 1, hd, dtype, 40)
+        idx[1, 0] = 1  # one row that does not name region 0 and one that does
+        idx[1, 1, 0] = 0
+        before = bra.diff_attend(q, k, v, idx, lam, 1, n_win)
+        v[1, 0, 0, 5] = float("inf")  # a token of region 0
+        out = bra.diff_attend(q, k, v, idx, lam, 1, n_win)
+        tok = ref.region_tokens(q.shape[1], q.shape[2], n_win)
+        named = torch.zeros(q.shape[1] * q.shape[2], dtype=torch.bool)
+        for r, t in enumerate(tok):
+            named[t] = bool((idx[1, r] == 0).any())
+        hit = torch.zeros(q.shape, dtype=torch.bool)
+        hit[1, :, :, 5] = named.view(q.shape[1], q.shape[2])
+        assert 0 < int(named.sum()) < named.numel()
+        assert not bool(torch.isfinite(out.cpu()[hit]).any())
+        assert torch.equal(out.cpu()[~hit], before.cpu()[~hit])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("spread", [0.0, 6.0, 1e-3])
 def test_flat_and_peaked_maps(dtype, spread):
     """All scores equal (spread 0), and scores some hundreds apart."""
