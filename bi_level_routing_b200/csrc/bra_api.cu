@@ -979,7 +979,7 @@ bra_status bra_norm_residual_backward(const void *x, const void *h, const void *
     a.dpre_b = dpre_bias;
     bra::norm_plan(a, true, st->num_sms);
     void *part = nullptr;
-    cudaError_t e = cudaMallocFromPoolAsync(&part, (size_t)a.units * 5 * C * sizeof(float), st->pool, cs);
+    cudaError_t e = cudaMallocFromPoolAsync(&part, (size_t)a.units * 4 * C * sizeof(float), st->pool, cs);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMallocFromPoolAsync(column sums)");
     a.part = static_cast<float *>(part);
     e = bra::launch_norm_residual(a, dtype == BRA_BF16, true, cs);

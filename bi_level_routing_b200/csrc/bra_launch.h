@@ -244,7 +244,7 @@ struct NormArgs {
     void *s, *y, *dx, *dh;
     const float *gate, *post_w, *post_b, *pre_w, *pre_b;
     float *dgate, *dpost_w, *dpost_b, *dpre_w, *dpre_b;
-    float *part;       // [units][5][C]
+    float *part;       // [units][4][C]
     int rows, images;  // rows of one image; images is 1 unless each has a gate of its own
     int C, nvec;       // 16-byte vectors of a row
     int chunks, per, units;

@@ -10,32 +10,33 @@
 //   dS = ds + N(dy w_pre, s^, r_s),  dx = alpha dS,  dp = gate dS,  dh = N(dp w_post, h^, r_h),
 //   dw_pre = sum dy s^, db_pre = sum dy, dgate = sum dS p, dw_post = sum dp h^, db_post = sum dp over rows.
 //
-// TPR threads hold one row in registers, VPT 16-byte vectors each; the next row's vectors load while
+// TPR threads hold one row in registers, VPT 16-byte vectors each; the next rows' vectors land in shared memory while
 // the current one is worked on. Means are taken before the squares about them (two sums, no
-// cancellation), all in fp32. The column sums of the backward pass stay in each thread's registers
-// over the rows of its CTA; the CTAs' sums go to a workspace and are added in a fixed order, so the
-// result is the same bits on every run.
+// cancellation), all in fp32. The weights and the gate are the same for every row of an image, so
+// four column sums give all their gradients: A = sum dS h^, S = sum dS, sum dy s^ and sum dy, with
+// dgate = w_post A + b_post S, dw_post = sum over images of gate A, db_post = of gate S (S and sum dy only where there is a
+// bias). They stay in each thread's registers over the rows of its CTA; the CTAs' sums go to a workspace and are added
+// in a fixed order, so the result is the same bits on every run.
 #include "bra_device.cuh"
+#include "bra_diff.cuh"
 #include "bra_launch.h"
 
 namespace bra {
 
 namespace {
 
-template <typename T, int VPT> struct RowVec {
-    static constexpr int V = Vec16<T>::N;
-    static constexpr int E = V * VPT;
-};
+// CTAs an SM in the forward pass: of 256 threads, and of 512
+constexpr int kForwardCtas = 3, kForwardWide = 1;
+constexpr int block_threads(int tpr) { return tpr > 256 ? tpr : 256; }
 
-// 16-byte loads that do not go through the read-only path (outputs may be the inputs' own buffers)
-__device__ __forceinline__ uint4 load16(const void *p)
-{
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
+// Row groups in the rings
+#ifndef FS
+#define FS 3
+#endif
+#ifndef BS
+#define BS 2
+#endif
+constexpr int kForwardStages = FS, kBackwardStages = BS;
 
 __device__ __forceinline__ uint4 pack16(const float (&f)[4], float)
 {
@@ -75,31 +76,63 @@ template <int TPR, int K> __device__ __forceinline__ void row_sums(float (&v)[K]
     }
 }
 
-// z becomes norm(z); returns 1 / sqrt(...). `valid` says which elements lie in the row (whole vectors).
+// Element-wise steps on pairs (the packed fp32 instructions halve what is issued).
+__device__ __forceinline__ float2 pair(const float *f) { return make_float2(f[0], f[1]); }
+__device__ __forceinline__ void put(float *f, float2 v)
+{
+    f[0] = v.x;
+    f[1] = v.y;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+template <int E> __device__ __forceinline__ void times(float (&z)[E], float r)
+{
+#pragma unroll
+    for (int i = 0; i < E; i += 2) put(z + i, __fmul2_rn(pair(z + i), both(r)));
+}
+template <int E> __device__ __forceinline__ void times(float (&z)[E], const float (&w)[E])
+{
+#pragma unroll
+    for (int i = 0; i < E; i += 2) put(z + i, __fmul2_rn(pair(z + i), pair(w + i)));
+}
+template <int E> __device__ __forceinline__ void plus(float (&z)[E], const float (&w)[E])
+{
+#pragma unroll
+    for (int i = 0; i < E; i += 2) put(z + i, __fadd2_rn(pair(z + i), pair(w + i)));
+}
+// z += x y
+template <int E> __device__ __forceinline__ void plus_product(float (&z)[E], const float (&x)[E], const float (&y)[E])
+{
+#pragma unroll
+    for (int i = 0; i < E; i += 2) put(z + i, __ffma2_rn(pair(x + i), pair(y + i), pair(z + i)));
+}
+
+// z becomes norm(z); returns 1 / sqrt(...). Elements past the row are 0 and stay so.
 template <int TPR, int V, int VPT>
 __device__ __forceinline__ float normalise(float (&z)[V * VPT], const NormArgs &a, int lane, float *red, int &turn)
 {
+    constexpr int E = V * VPT;
     float sum[1];
     if (a.layer) {
-        sum[0] = 0.f;
+        float2 t = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < V * VPT; ++i) sum[0] += z[i];  // elements past the row are 0
+        for (int i = 0; i < E; i += 2) t = __fadd2_rn(t, pair(z + i));
+        sum[0] = t.x + t.y;
         row_sums<TPR, 1>(sum, red, turn);
         const float mean = sum[0] * a.inv_c;
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
             if (lane + i * TPR < a.nvec) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) z[i * V + j] -= mean;
+                for (int j = 0; j < V; j += 2) put(z + i * V + j, __fadd2_rn(pair(z + i * V + j), both(-mean)));
             }
     }
-    sum[0] = 0.f;
+    float2 t = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < V * VPT; ++i) sum[0] = fmaf(z[i], z[i], sum[0]);
+    for (int i = 0; i < E; i += 2) t = __ffma2_rn(pair(z + i), pair(z + i), t);
+    sum[0] = t.x + t.y;
     row_sums<TPR, 1>(sum, red, turn);
     const float r = 1.f / sqrtf(fmaf(sum[0], a.inv_c, a.eps));
-#pragma unroll
-    for (int i = 0; i < V * VPT; ++i) z[i] *= r;
+    times(z, r);
     return r;
 }
 
@@ -108,16 +141,17 @@ __device__ __forceinline__ float normalise(float (&z)[V * VPT], const NormArgs &
 template <int TPR, int E>
 __device__ __forceinline__ void norm_back(float (&u)[E], const float (&z)[E], float r, const NormArgs &a, float *red, int &turn)
 {
-    float sum[2] = {0.f, 0.f};
+    float2 t0 = make_float2(0.f, 0.f), t1 = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        sum[0] += u[i];
-        sum[1] = fmaf(u[i], z[i], sum[1]);
+    for (int i = 0; i < E; i += 2) {
+        t0 = __fadd2_rn(t0, pair(u + i));
+        t1 = __ffma2_rn(pair(u + i), pair(z + i), t1);
     }
+    float sum[2] = {t0.x + t0.y, t1.x + t1.y};
     row_sums<TPR, 2>(sum, red, turn);
-    const float m0 = a.layer ? sum[0] * a.inv_c : 0.f, m1 = sum[1] * a.inv_c;
+    const float2 m0 = both(a.layer ? -r * sum[0] * a.inv_c : 0.f), m1 = both(-r * sum[1] * a.inv_c), rr = both(r);
 #pragma unroll
-    for (int i = 0; i < E; ++i) u[i] = r * (u[i] - m0 - z[i] * m1);
+    for (int i = 0; i < E; i += 2) put(u + i, __ffma2_rn(pair(z + i), m1, __ffma2_rn(pair(u + i), rr, m0)));
 }
 
 // E values of a channel array at this thread's vectors; `def` where the array is absent or past the row.
@@ -137,16 +171,91 @@ __device__ __forceinline__ void load_channels(float (&w)[V * VPT], const float *
         }
 }
 
-template <typename T, int TPR, int VPT>
-__device__ __forceinline__ void load_row(uint4 (&raw)[VPT], const void *base, int64_t row, const NormArgs &a, int lane, bool in)
+// The branch's factor gate * w_post and offset gate * b_post: p = h^ gw + gb.
+template <int TPR, int V, int VPT>
+__device__ __forceinline__ void load_branch(float (&w)[V * VPT], const float *gate, const float *p, float def, int nvec, int lane)
 {
+    load_channels<TPR, V, VPT>(w, p, def, nvec, lane);
+    if (gate) {
+        float g[V * VPT];
+        load_channels<TPR, V, VPT>(g, gate, 1.f, nvec, lane);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (in && base && lane + i * TPR < a.nvec)
-            raw[i] = load16(static_cast<const T *>(base) + row * a.C + (int64_t)(lane + i * TPR) * Vec16<T>::N);
+        for (int i = 0; i < V * VPT; ++i) w[i] *= g[i];
     }
 }
+
+// A ring of STAGES row groups of ARRAYS input arrays in shared memory. Every thread copies the vectors it will itself read
+// (cp.async, no barrier), STAGES - 1 groups ahead: registers could hold one group, too few bytes in flight for
+// the memory's latency.
+template <typename T, int TPR, int VPT, int ARRAYS, int WANTED> struct RowRing {
+    static constexpr int kThreads = block_threads(TPR);
+    static constexpr int kGroup = ARRAYS * VPT * kThreads * 16;
+    // the widest fp32 rows leave room for fewer: one, if need be, which is copied when it is wanted
+    static constexpr int kRoom = 226 * 1024 - (VPT > 1 ? 2 * Vec16<T>::N * VPT * kThreads * 4 : 0);
+    static constexpr int kFit = kRoom / kGroup, STAGES = kFit < 1 ? 1 : kFit < WANTED ? kFit : WANTED;
+    static constexpr int kAhead = STAGES - 1;
+    static constexpr size_t kBytes = (size_t)STAGES * kGroup;
+    static_assert(kBytes <= kRoom, "one row group must fit");
+    const NormArgs &a;
+    const void *base[ARRAYS];
+    uint8_t *mine;
+    int lane, put = 0, get = 0;
+
+    __device__ __forceinline__ RowRing(const NormArgs &args, uint8_t *smem, int row_lane)
+        : a(args), mine(smem + threadIdx.x * 16), lane(row_lane) {}
+    __device__ __forceinline__ uint8_t *slot(int stage, int array, int i) const
+    {
+        return mine + (size_t)((stage * ARRAYS + array) * VPT + i) * (kThreads * 16);
+    }
+    // copies row `row` (zeros where it is not one, or an array is absent) and commits
+    __device__ __forceinline__ void fetch(int64_t row, bool in)
+    {
+#pragma unroll
+        for (int k = 0; k < ARRAYS; ++k)
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const bool real = in && base[k] && lane + i * TPR < a.nvec;
+                const T *src = static_cast<const T *>(real ? base[k] : a.x);
+                if (real) src += row * a.C + (int64_t)(lane + i * TPR) * Vec16<T>::N;
+                cp_async16_or_zero(smem_u32(slot(put, k, i)), src, real);
+            }
+        cp_async_commit();
+        put = put + 1 == STAGES ? 0 : put + 1;
+    }
+    __device__ __forceinline__ void wait() { cp_async_wait_but<(STAGES > 1 ? STAGES - 2 : 0)>(); }
+    __device__ __forceinline__ void read(int k, float (&f)[Vec16<T>::N * VPT]) const
+    {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) Vec16<T>::unpack(*reinterpret_cast<const uint4 *>(slot(get, k, i)), f + i * Vec16<T>::N);
+    }
+    __device__ __forceinline__ void next() { get = get + 1 == STAGES ? 0 : get + 1; }
+};
+
+// Two channel arrays in shared memory, each thread's own elements where it reads them itself (no barrier): what wide rows
+// cannot keep in registers.
+template <int TPR, int E> struct Stash {
+    static constexpr int kThreads = block_threads(TPR);
+    static constexpr size_t kBytes = (size_t)2 * E * kThreads * sizeof(float);
+    float4 *mine;
+    __device__ __forceinline__ explicit Stash(float *smem) : mine(reinterpret_cast<float4 *>(smem) + threadIdx.x) {}
+    __device__ __forceinline__ void write(int k, const float (&w)[E])
+    {
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i)
+            mine[(k * (E / 4) + i) * kThreads] = make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    __device__ __forceinline__ void read(int k, float (&w)[E]) const
+    {
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) {
+            const float4 f = mine[(k * (E / 4) + i) * kThreads];
+            w[4 * i] = f.x;
+            w[4 * i + 1] = f.y;
+            w[4 * i + 2] = f.z;
+            w[4 * i + 3] = f.w;
+        }
+    }
+};
 
 template <typename T, int TPR, int VPT>
 __device__ __forceinline__ void store_row(void *base, int64_t row, const NormArgs &a, int lane, const float (&f)[Vec16<T>::N * VPT])
@@ -162,22 +271,16 @@ __device__ __forceinline__ void store_row(void *base, int64_t row, const NormArg
         }
 }
 
-template <typename T, int VPT> __device__ __forceinline__ void unpack_row(const uint4 (&raw)[VPT], float (&f)[Vec16<T>::N * VPT])
-{
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) Vec16<T>::unpack(raw[i], f + i * Vec16<T>::N);
-}
-
-constexpr int block_threads(int tpr) { return tpr > 256 ? tpr : 256; }
-
 }  // namespace
 
 template <typename T, int TPR, int VPT>
-__global__ void __launch_bounds__(block_threads(TPR)) norm_residual_kernel(const NormArgs a)
+__global__ void __launch_bounds__(block_threads(TPR), TPR > 256 ? kForwardWide : kForwardCtas) norm_residual_kernel(const NormArgs a)
 {
     constexpr int V = Vec16<T>::N, E = V * VPT, RPC = block_threads(TPR) / TPR;
-    constexpr bool kKeep = E <= 8;  // the channel arrays stay in registers (5 E of them); else they come from L1
-    __shared__ float red[128];
+    constexpr bool kKeep = E <= 8;  // the channel arrays stay in registers (4 E of them); else they come from L1
+    extern __shared__ float4 smem4[];
+    using Ring = RowRing<T, TPR, VPT, 2, kForwardStages>;
+    float *red = reinterpret_cast<float *>(smem4) + Ring::kBytes / 4;
     const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR;
     const int image = blockIdx.x / a.chunks, chunk = blockIdx.x - image * a.chunks;
     const int64_t row0 = (int64_t)image * a.rows;
@@ -185,87 +288,91 @@ __global__ void __launch_bounds__(block_threads(TPR)) norm_residual_kernel(const
     const float *gate = a.gate ? a.gate + (a.gate_images ? (int64_t)image * a.C : 0) : nullptr;
     int turn = 0;
     grid_dependency_wait();
-    float wg[kKeep ? E : 1], wp[kKeep ? E : 1], bp[kKeep ? E : 1], wn[kKeep ? E : 1], bn[kKeep ? E : 1];
+    Ring ring(a, reinterpret_cast<uint8_t *>(smem4), lane);
+    ring.base[0] = a.x;
+    ring.base[1] = a.h;
+#pragma unroll
+    for (int k = 0; k < Ring::kAhead; ++k) ring.fetch(row0 + begin + k * RPC + grp, begin + k * RPC + grp < end);
+    Stash<TPR, E> stash(red + 128);
+    float w[kKeep ? 4 : 1][E];  // gate w_post, gate b_post, w_pre, b_pre
     if constexpr (kKeep) {
-        load_channels<TPR, V, VPT>(wg, gate, 1.f, a.nvec, lane);
-        load_channels<TPR, V, VPT>(wp, a.post_w, 1.f, a.nvec, lane);
-        load_channels<TPR, V, VPT>(bp, a.post_b, 0.f, a.nvec, lane);
-        load_channels<TPR, V, VPT>(wn, a.pre_w, 1.f, a.nvec, lane);
-        load_channels<TPR, V, VPT>(bn, a.pre_b, 0.f, a.nvec, lane);
+        if (a.h) {
+            load_branch<TPR, V, VPT>(w[0], gate, a.post_w, 1.f, a.nvec, lane);
+            load_branch<TPR, V, VPT>(w[1], a.post_b ? gate : nullptr, a.post_b, 0.f, a.nvec, lane);
+        }
+        if (a.pre_w) {
+            load_channels<TPR, V, VPT>(w[2], a.pre_w, 1.f, a.nvec, lane);
+            load_channels<TPR, V, VPT>(w[3], a.pre_b, 0.f, a.nvec, lane);
+        }
+    } else {
+        if (a.h) {
+            load_branch<TPR, V, VPT>(w[0], gate, a.post_w, 1.f, a.nvec, lane);
+            stash.write(0, w[0]);
+        }
+        if (a.pre_w) {
+            load_channels<TPR, V, VPT>(w[0], a.pre_w, 1.f, a.nvec, lane);
+            stash.write(1, w[0]);
+        }
     }
-    uint4 xr[VPT], hr[VPT];
-    load_row<T, TPR, VPT>(xr, a.x, row0 + begin + grp, a, lane, begin + grp < end);
-    load_row<T, TPR, VPT>(hr, a.h, row0 + begin + grp, a, lane, begin + grp < end);
     for (int r = begin; r < end; r += RPC) {
         const int64_t row = row0 + r + grp;
         const bool in = r + grp < end;
-        float s[E], p[E];
-        unpack_row<T, VPT>(xr, s);
-        unpack_row<T, VPT>(hr, p);
-        const bool more = r + RPC + grp < end;
-        load_row<T, TPR, VPT>(xr, a.x, row + RPC, a, lane, more);
-        load_row<T, TPR, VPT>(hr, a.h, row + RPC, a, lane, more);
+        float s[E];
+        if (Ring::kAhead == 0) ring.fetch(row, in);
+        ring.wait();
+        ring.read(0, s);
+#pragma unroll
+        for (int i = 0; i < E; ++i) s[i] *= a.alpha;
         if (a.h) {
-            if (a.post_w) {
-                normalise<TPR, V, VPT>(p, a, lane, red, turn);
-                if constexpr (kKeep) {
+            float p[E];
+            ring.read(1, p);
+            if (a.post_w) normalise<TPR, V, VPT>(p, a, lane, red, turn);
+            if constexpr (kKeep) {
 #pragma unroll
-                    for (int i = 0; i < E; ++i) p[i] = fmaf(p[i], wp[i], bp[i]);
-                } else {
-                    float w[E];
-                    load_channels<TPR, V, VPT>(w, a.post_w, 1.f, a.nvec, lane);
+                for (int i = 0; i < E; ++i) s[i] += fmaf(p[i], w[0][i], w[1][i]);
+            } else {
+                load_branch<TPR, V, VPT>(w[0], gate, a.post_w, 1.f, a.nvec, lane);
 #pragma unroll
-                    for (int i = 0; i < E; ++i) p[i] *= w[i];
-                    if (a.post_b) {
-                        load_channels<TPR, V, VPT>(w, a.post_b, 0.f, a.nvec, lane);
+                for (int i = 0; i < E; ++i) s[i] = fmaf(p[i], w[0][i], s[i]);
+                if (a.post_b) {
+                    load_branch<TPR, V, VPT>(w[0], gate, a.post_b, 0.f, a.nvec, lane);
 #pragma unroll
-                        for (int i = 0; i < E; ++i) p[i] += w[i];
-                    }
-                }
-            }
-            if (gate) {
-                if constexpr (kKeep) {
-#pragma unroll
-                    for (int i = 0; i < E; ++i) p[i] *= wg[i];
-                } else {
-                    float w[E];
-                    load_channels<TPR, V, VPT>(w, gate, 1.f, a.nvec, lane);
-#pragma unroll
-                    for (int i = 0; i < E; ++i) p[i] *= w[i];
+                    for (int i = 0; i < E; ++i) s[i] += w[0][i];
                 }
             }
         }
-#pragma unroll
-        for (int i = 0; i < E; ++i) s[i] = fmaf(a.alpha, s[i], p[i]);
+        ring.next();
+        if (Ring::kAhead > 0) ring.fetch(row + Ring::kAhead * RPC, r + Ring::kAhead * RPC + grp < end);
         if (a.s && in) store_row<T, TPR, VPT>(a.s, row, a, lane, s);
         if (a.pre_w) {
             normalise<TPR, V, VPT>(s, a, lane, red, turn);
             if constexpr (kKeep) {
-#pragma unroll
-                for (int i = 0; i < E; ++i) s[i] = fmaf(s[i], wn[i], bn[i]);
+                times(s, w[2]);
+                plus(s, w[3]);
             } else {
-                float w[E];
-                load_channels<TPR, V, VPT>(w, a.pre_w, 1.f, a.nvec, lane);
-#pragma unroll
-                for (int i = 0; i < E; ++i) s[i] *= w[i];
+                stash.read(1, w[0]);
+                times(s, w[0]);
                 if (a.pre_b) {
-                    load_channels<TPR, V, VPT>(w, a.pre_b, 0.f, a.nvec, lane);
-#pragma unroll
-                    for (int i = 0; i < E; ++i) s[i] += w[i];
+                    load_channels<TPR, V, VPT>(w[0], a.pre_b, 0.f, a.nvec, lane);
+                    plus(s, w[0]);
                 }
             }
             if (in) store_row<T, TPR, VPT>(a.y, row, a, lane, s);
         }
     }
+    cp_async_wait_all();
 }
 
-// part [units][5][C]: each CTA's column sums dw_post, db_post, dw_pre, db_pre, dgate
-template <typename T, int TPR, int VPT>
-__global__ void __launch_bounds__(block_threads(TPR)) norm_residual_backward_kernel(const NormArgs a)
+// part [units][4][C]: each CTA's column sums A, sum dy s^, S, sum dy (the last two where BIAS)
+template <typename T, int TPR, int VPT, bool BIAS>
+__global__ void __launch_bounds__(block_threads(TPR), TPR > 256 ? 1 : 2) norm_residual_backward_kernel(const NormArgs a)
 {
     constexpr int V = Vec16<T>::N, E = V * VPT, RPC = block_threads(TPR) / TPR, THREADS = block_threads(TPR);
-    __shared__ float red[128];
+    constexpr int SUMS = BIAS ? 4 : 2;
+    constexpr bool kKeep = VPT == 1;  // the channel arrays stay in registers
     extern __shared__ float4 smem4[];
+    using Ring = RowRing<T, TPR, VPT, 4, kBackwardStages>;
+    float *red = reinterpret_cast<float *>(smem4) + Ring::kBytes / 4;
     const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR;
     const int image = blockIdx.x / a.chunks, chunk = blockIdx.x - image * a.chunks;
     const int64_t row0 = (int64_t)image * a.rows;
@@ -273,101 +380,102 @@ __global__ void __launch_bounds__(block_threads(TPR)) norm_residual_backward_ker
     const float *gate = a.gate ? a.gate + (a.gate_images ? (int64_t)image * a.C : 0) : nullptr;
     int turn = 0;
     grid_dependency_wait();
-    float sum[5][E];
+    Ring ring(a, reinterpret_cast<uint8_t *>(smem4), lane);
+    ring.base[0] = a.x;
+    ring.base[1] = a.h;
+    ring.base[2] = a.dy;
+    ring.base[3] = a.ds;
 #pragma unroll
-    for (int k = 0; k < 5; ++k)
+    for (int k = 0; k < Ring::kAhead; ++k) ring.fetch(row0 + begin + k * RPC + grp, begin + k * RPC + grp < end);
+    float sum[SUMS][E];
+#pragma unroll
+    for (int k = 0; k < SUMS; ++k)
 #pragma unroll
         for (int i = 0; i < E; ++i) sum[k][i] = 0.f;
-    uint4 xr[VPT], hr[VPT], yr[VPT], sr[VPT];
-    auto load_all = [&](int64_t row, bool in) {
-        load_row<T, TPR, VPT>(xr, a.x, row, a, lane, in);
-        load_row<T, TPR, VPT>(hr, a.h, row, a, lane, in);
-        load_row<T, TPR, VPT>(yr, a.dy, row, a, lane, in);
-        load_row<T, TPR, VPT>(sr, a.ds, row, a, lane, in);
-    };
-    load_all(row0 + begin + grp, begin + grp < end);
+    Stash<TPR, E> stash(red + 128);
+    float gw[E], gb[kKeep && BIAS ? E : 1], wn[kKeep ? E : 1];
+    if constexpr (kKeep) {
+        if (a.h) {
+            load_branch<TPR, V, VPT>(gw, gate, a.post_w, 1.f, a.nvec, lane);
+            if constexpr (BIAS) load_branch<TPR, V, VPT>(gb, a.post_b ? gate : nullptr, a.post_b, 0.f, a.nvec, lane);
+        }
+        if (a.pre_w) load_channels<TPR, V, VPT>(wn, a.pre_w, 0.f, a.nvec, lane);
+    } else {
+        if (a.h) {
+            load_branch<TPR, V, VPT>(gw, gate, a.post_w, 1.f, a.nvec, lane);
+            stash.write(0, gw);
+        }
+        if (a.pre_w) {
+            load_channels<TPR, V, VPT>(gw, a.pre_w, 0.f, a.nvec, lane);
+            stash.write(1, gw);
+        }
+    }
     for (int r = begin; r < end; r += RPC) {
         const int64_t row = row0 + r + grp;
         const bool in = r + grp < end;
-        float s[E], hn[E], u[E], dS[E], w[E];
-        unpack_row<T, VPT>(xr, s);
-        unpack_row<T, VPT>(hr, hn);
-        unpack_row<T, VPT>(yr, u);
-        unpack_row<T, VPT>(sr, dS);
-        load_all(row + RPC, r + RPC + grp < end);
-        // the forward pass again: hn = norm(h) (or h), s = alpha x + gate p
+        if (Ring::kAhead == 0) ring.fetch(row, in);
+        ring.wait();
+        // the forward pass again: hn = norm(h) (or h), s = alpha x + hn gw + gb
+        float s[E], hn[E];
+        ring.read(0, s);
+        times(s, a.alpha);
         float rh = 1.f;
-        if (a.h && a.post_w) rh = normalise<TPR, V, VPT>(hn, a, lane, red, turn);
-        auto branch = [&](float (&p)[E]) {  // p = hn w_post + b_post
-            if (a.post_w) {
-                load_channels<TPR, V, VPT>(w, a.post_w, 0.f, a.nvec, lane);
-#pragma unroll
-                for (int i = 0; i < E; ++i) p[i] = hn[i] * w[i];
-                if (a.post_b) {
-                    load_channels<TPR, V, VPT>(w, a.post_b, 0.f, a.nvec, lane);
-#pragma unroll
-                    for (int i = 0; i < E; ++i) p[i] += w[i];
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < E; ++i) p[i] = hn[i];
+        if (a.h) {
+            ring.read(1, hn);
+            if (a.post_w) rh = normalise<TPR, V, VPT>(hn, a, lane, red, turn);
+            if (!kKeep) stash.read(0, gw);
+            plus_product(s, hn, gw);
+            if constexpr (BIAS && kKeep) {
+                plus(s, gb);
+            } else if (BIAS && a.post_b) {
+                load_branch<TPR, V, VPT>(gw, gate, a.post_b, 0.f, a.nvec, lane);
+                plus(s, gw);
             }
-        };
-        float p[E];
-        branch(p);
-        if (gate) load_channels<TPR, V, VPT>(w, gate, 0.f, a.nvec, lane);
-#pragma unroll
-        for (int i = 0; i < E; ++i) s[i] = fmaf(a.alpha, s[i], gate ? w[i] * p[i] : p[i]);
+        }
+        float dS[E];
         if (a.pre_w) {
             const float rs = normalise<TPR, V, VPT>(s, a, lane, red, turn);
+            ring.read(2, dS);
             if (in) {
-#pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    sum[2][i] = fmaf(u[i], s[i], sum[2][i]);
-                    sum[3][i] += u[i];
-                }
+                plus_product(sum[1], dS, s);
+                if (BIAS) plus(sum[SUMS - 1], dS);
             }
-            load_channels<TPR, V, VPT>(w, a.pre_w, 0.f, a.nvec, lane);
+            if constexpr (kKeep) {
+                times(dS, wn);
+            } else {
+                stash.read(1, gw);
+                times(dS, gw);
+            }
+            norm_back<TPR, E>(dS, s, rs, a, red, turn);
+        } else {
 #pragma unroll
-            for (int i = 0; i < E; ++i) u[i] *= w[i];
-            norm_back<TPR, E>(u, s, rs, a, red, turn);
-#pragma unroll
-            for (int i = 0; i < E; ++i) dS[i] += u[i];
+            for (int i = 0; i < E; ++i) dS[i] = 0.f;
         }
-        float dx[E];
+        ring.read(3, s);
+        ring.next();
+        if (Ring::kAhead > 0) ring.fetch(row + Ring::kAhead * RPC, r + Ring::kAhead * RPC + grp < end);
+        plus(dS, s);
 #pragma unroll
-        for (int i = 0; i < E; ++i) dx[i] = a.alpha * dS[i];
-        if (in) store_row<T, TPR, VPT>(a.dx, row, a, lane, dx);
+        for (int i = 0; i < E; ++i) s[i] = dS[i];
+        times(s, a.alpha);
+        if (in) store_row<T, TPR, VPT>(a.dx, row, a, lane, s);
         if (a.h) {
-            if (gate) {
-                load_channels<TPR, V, VPT>(w, gate, 0.f, a.nvec, lane);
-#pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    if (in) sum[4][i] = fmaf(dS[i], p[i], sum[4][i]);
-                    dS[i] *= w[i];
-                }
+            if (in) {
+                plus_product(sum[0], dS, hn);
+                if (BIAS) plus(sum[SUMS - 2], dS);
             }
-            if (a.post_w) {
-                if (in) {
-#pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        sum[0][i] = fmaf(dS[i], hn[i], sum[0][i]);
-                        sum[1][i] += dS[i];
-                    }
-                }
-                load_channels<TPR, V, VPT>(w, a.post_w, 0.f, a.nvec, lane);
-#pragma unroll
-                for (int i = 0; i < E; ++i) dS[i] *= w[i];
-                norm_back<TPR, E>(dS, hn, rh, a, red, turn);
-            }
+            if (!kKeep) stash.read(0, gw);
+            times(dS, gw);
+            if (a.post_w) norm_back<TPR, E>(dS, hn, rh, a, red, turn);
             if (in) store_row<T, TPR, VPT>(a.dh, row, a, lane, dS);
         }
     }
-    // the CTA's sums: row groups meet in shared memory, a few groups' worth of columns at a time
+    cp_async_wait_all();
+    // the CTA's sums: row groups meet in shared memory
     float *buf = reinterpret_cast<float *>(smem4);
-    float *part = a.part + (int64_t)blockIdx.x * 5 * a.C;
+    float *part = a.part + (int64_t)blockIdx.x * 4 * a.C;
 #pragma unroll
-    for (int k = 0; k < 5; ++k) {
+    for (int k = 0; k < SUMS; ++k) {
         if (RPC > 1) {
             __syncthreads();
 #pragma unroll
@@ -388,31 +496,67 @@ __global__ void __launch_bounds__(block_threads(TPR)) norm_residual_backward_ker
     }
 }
 
-// Adds the units' column sums, 32 channels and 8 runs of units to a CTA. blockIdx.y: the four weight
-// arrays, then the gate (one for each image where it has one).
-__global__ void __launch_bounds__(256) norm_column_sums_kernel(const NormArgs a)
+// The gradients of the weights and the gate from the units' column sums, 32 channels and kRuns runs of images (or, with one
+// gate, of units) to a CTA. Few CTAs of many threads: what it takes is the latency of its loads.
+constexpr int kRuns = 32;
+
+__global__ void __launch_bounds__(32 * kRuns) norm_column_sums_kernel(const NormArgs a)
 {
-    __shared__ double sums[8][32];
-    const int c = blockIdx.x * 32 + threadIdx.x % 32, run = threadIdx.x / 32;
-    const int y = blockIdx.y;
-    float *dst = y == 0 ? a.dpost_w : y == 1 ? a.dpost_b : y == 2 ? a.dpre_w : y == 3 ? a.dpre_b : a.dgate;
+    __shared__ double sums[4][kRuns][32];
+    const int lane = threadIdx.x % 32, c = blockIdx.x * 32 + lane, run = threadIdx.x / 32;
+    const bool in = c < a.C;
+    const bool bias = a.post_b || a.pre_b;
+    double total[4] = {0., 0., 0., 0.};  // sum gate A, sum dy s^, sum gate S, sum dy
     grid_dependency_wait();
-    if (!dst) return;
-    int u0 = 0, u1 = a.units;
-    if (y >= 4 && a.gate_images) {
-        u0 = (y - 4) * a.chunks;
-        u1 = u0 + a.chunks;
-        dst += (int64_t)(y - 4) * a.C;
+    if (in) {
+        const float w = a.post_w ? __ldg(a.post_w + c) : 1.f, b = a.post_b ? __ldg(a.post_b + c) : 0.f;
+        if (a.gate_images) {
+            for (int image = run; image < a.images; image += kRuns) {
+                const float g = __ldg(a.gate + (int64_t)image * a.C + c);
+                double x[4] = {0., 0., 0., 0.};
+#pragma unroll 4
+                for (int u = image * a.chunks; u < (image + 1) * a.chunks; ++u)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < 2 || bias) x[k] += (double)__ldcg(a.part + ((int64_t)u * 4 + k) * a.C + c);
+                a.dgate[(int64_t)image * a.C + c] = (float)(w * x[0] + b * x[2]);
+                total[0] += g * x[0];
+                total[1] += x[1];
+                total[2] += g * x[2];
+                total[3] += x[3];
+            }
+        } else {
+#pragma unroll 4
+            for (int u = run; u < a.units; u += kRuns)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k < 2 || bias) total[k] += (double)__ldcg(a.part + ((int64_t)u * 4 + k) * a.C + c);
+        }
     }
-    const float *src = a.part + (int64_t)(y < 4 ? y : 4) * a.C;
-    double sum = 0.;
-    if (c < a.C)
-        for (int u = u0 + run; u < u1; u += 8) sum += (double)__ldcg(src + (int64_t)u * 5 * a.C + c);
-    sums[run][threadIdx.x % 32] = sum;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sums[k][run][lane] = total[k];
     __syncthreads();
-    if (run == 0 && c < a.C) {
-        for (int i = 1; i < 8; ++i) sum += sums[i][threadIdx.x];
-        dst[c] = (float)sum;
+    if (run < 4) {  // warp k adds array k
+        double all = 0.;
+#pragma unroll 8
+        for (int i = 0; i < kRuns; ++i) all += sums[run][i][lane];
+        sums[run][0][lane] = all;
+    }
+    __syncthreads();
+    if (run == 0 && in) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) total[k] = sums[k][0][lane];
+        if (!a.gate_images) {
+            const float g = a.gate ? __ldg(a.gate + c) : 1.f;
+            const float w = a.post_w ? __ldg(a.post_w + c) : 1.f, b = a.post_b ? __ldg(a.post_b + c) : 0.f;
+            if (a.dgate) a.dgate[c] = (float)(w * total[0] + b * total[2]);
+            total[0] *= g;
+            total[2] *= g;
+        }
+        if (a.dpost_w) a.dpost_w[c] = (float)total[0];
+        if (a.dpre_w) a.dpre_w[c] = (float)total[1];
+        if (a.dpost_b) a.dpost_b[c] = (float)total[2];
+        if (a.dpre_b) a.dpre_b[c] = (float)total[3];
     }
 }
 
@@ -420,22 +564,23 @@ bool norm_supports(int C, bool bf16) { return C % (bf16 ? 8 : 4) == 0 && C <= 81
 
 namespace {
 
-// Threads a row and vectors a thread: whole warps' worth of short rows, at most two vectors a thread
-// (four in fp32, whose vectors hold half as many channels).
+// Threads a row and vectors a thread: a vector a thread up to 256 threads, then two, so that several CTAs share an SM and
+// one works while another waits for its rows' sums; 512 threads for the widest rows.
 void row_shape(int nvec, int &tpr, int &vpt)
 {
     tpr = 4;
-    while (tpr < nvec && tpr < 512) tpr *= 2;
+    while (tpr < nvec && tpr < 256) tpr *= 2;
+    if (nvec > 512) tpr = 512;
     vpt = (nvec + tpr - 1) / tpr;
     if (vpt == 3) vpt = 4;
 }
 
-// CTAs: whole rounds of the GPU, each a run of whole row groups of one image (of the whole batch where
-// no image has a gate of its own).
+// CTAs of one round of the GPU, each a run of whole row groups of one image (of the whole batch where no image has a
+// gate of its own).
 void split_rows(NormArgs &a, int threads, int tpr, int ctas)
 {
     const int rpc = threads / tpr;
-    long long chunks = (ctas + a.images - 1) / a.images;
+    long long chunks = ctas / a.images;
     const long long most = (a.rows + rpc - 1) / rpc;
     if (chunks > most) chunks = most;
     if (chunks < 1) chunks = 1;
@@ -445,15 +590,29 @@ void split_rows(NormArgs &a, int threads, int tpr, int ctas)
     a.units = a.chunks * a.images;
 }
 
+template <auto Kernel> cudaError_t launch_with(int threads, size_t smem, const NormArgs &a, cudaStream_t stream)
+{
+    const cudaError_t e = grant_shared_memory<Kernel>();
+    return e == cudaSuccess ? launch_pdl(Kernel, dim3(a.units), dim3(threads), smem, stream, a) : e;
+}
+
 template <typename T, int TPR, int VPT> cudaError_t launch_norm(const NormArgs &a, bool backward, cudaStream_t stream)
 {
     constexpr int threads = block_threads(TPR);
-    if (!backward) return launch_pdl(norm_residual_kernel<T, TPR, VPT>, dim3(a.units), dim3(threads), 0, stream, a);
-    const size_t smem = threads > TPR ? sizeof(float) * Vec16<T>::N * VPT * threads : 0;
-    cudaError_t e = launch_pdl(norm_residual_backward_kernel<T, TPR, VPT>, dim3(a.units), dim3(threads), smem, stream, a);
+    constexpr int E = Vec16<T>::N * VPT;
+    constexpr size_t red = 128 * sizeof(float) + (E > 8 || (VPT > 1) ? Stash<TPR, E>::kBytes : 0);
+    if (!backward)
+        return launch_with<norm_residual_kernel<T, TPR, VPT>>(
+            threads, RowRing<T, TPR, VPT, 2, kForwardStages>::kBytes + red, a, stream);
+    // the ring, later the row groups' column sums
+    constexpr size_t ring = RowRing<T, TPR, VPT, 4, kBackwardStages>::kBytes;
+    constexpr size_t sums = threads > TPR ? sizeof(float) * Vec16<T>::N * VPT * threads : 0;
+    constexpr size_t smem = (ring > sums ? ring : sums) + red;
+    cudaError_t e = a.post_b || a.pre_b
+                        ? launch_with<norm_residual_backward_kernel<T, TPR, VPT, true>>(threads, smem, a, stream)
+                        : launch_with<norm_residual_backward_kernel<T, TPR, VPT, false>>(threads, smem, a, stream);
     if (e != cudaSuccess) return e;
-    return launch_pdl(norm_column_sums_kernel, dim3((a.C + 31) / 32, 4 + (a.gate_images ? a.images : 1)), dim3(256), 0,
-                      stream, a);
+    return launch_pdl(norm_column_sums_kernel, dim3((a.C + 31) / 32), dim3(32 * kRuns), 0, stream, a);
 }
 
 template <typename T> cudaError_t launch_norm_t(const NormArgs &a, int tpr, int vpt, bool backward, cudaStream_t stream)
@@ -465,10 +624,9 @@ template <typename T> cudaError_t launch_norm_t(const NormArgs &a, int tpr, int 
     case 32: return launch_norm<T, 32, 1>(a, backward, stream);
     case 64: return launch_norm<T, 64, 1>(a, backward, stream);
     case 128: return launch_norm<T, 128, 1>(a, backward, stream);
-    case 256: return launch_norm<T, 256, 1>(a, backward, stream);
+    case 256: return vpt == 1 ? launch_norm<T, 256, 1>(a, backward, stream) : launch_norm<T, 256, 2>(a, backward, stream);
     default: break;
     }
-    if (vpt == 1) return launch_norm<T, 512, 1>(a, backward, stream);
     if (vpt == 2) return launch_norm<T, 512, 2>(a, backward, stream);
     if constexpr (Vec16<T>::N == 4) return launch_norm<T, 512, 4>(a, backward, stream);
     return cudaErrorInvalidConfiguration;
@@ -481,7 +639,8 @@ void norm_plan(NormArgs &a, bool backward, int num_sms)
     int tpr, vpt;
     row_shape(a.nvec, tpr, vpt);
     const int threads = block_threads(tpr);
-    split_rows(a, threads, tpr, num_sms * (backward ? (threads > 256 ? 1 : 2) : 2048 / threads));
+    // CTAs that an SM holds: the kernels' launch bounds
+    split_rows(a, threads, tpr, num_sms * (threads > 256 ? (backward ? 1 : kForwardWide) : backward ? 2 : kForwardCtas));
 }
 
 cudaError_t launch_norm_residual(const NormArgs &a, bool bf16, bool backward, cudaStream_t stream)

@@ -262,7 +262,7 @@ bra_status bra_norm_residual(const void *x, const void *h, const float *gate, in
    exactly where pre_weight is; ds NULL counts as 0 (one of the two is given). dx and, where h is given,
    dh: device [B, H, W, C] of dtype, written; distinct, and may be one of x, h, dy, ds themselves. The weights'
    gradients (device fp32, of their weights' shapes; each given exactly where its weight is) are summed in a
-   fixed order, the same bits on every run; for B == 0 they are 0. Takes scratch from the pool: 20 C
+   fixed order, the same bits on every run; for B == 0 they are 0. Takes scratch from the pool: 16 C
    bytes for each CTA of the launch. */
 bra_status bra_norm_residual_backward(const void *x, const void *h, const void *dy, const void *ds, const float *gate,
                                       int gate_images, const float *post_weight, const float *post_bias,
