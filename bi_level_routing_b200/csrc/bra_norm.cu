@@ -112,6 +112,32 @@ __device__ __forceinline__ float normalise(float (&z)[V * VPT], const NormArgs &
 {
     constexpr int E = V * VPT;
     float sum[1];
+    if (a.layer && TPR <= 32 && a.nvec == TPR * VPT) {
+        // Every thread holds E elements: mean and squares about it, merged pair by pair (two sets of n elements with means x and
+        // y: the mean (x + y) / 2, the squares' sum grown by (x - y)^2 n / 2), one chain of exchanges instead of two.
+        float2 t = make_float2(0.f, 0.f), q = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < E; i += 2) t = __fadd2_rn(t, pair(z + i));
+        float mean = (t.x + t.y) * (1.f / E);
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+            const float2 d = __fadd2_rn(pair(z + i), both(-mean));
+            q = __ffma2_rn(d, d, q);
+        }
+        float squares = q.x + q.y;
+#pragma unroll
+        for (int o = 1; o < TPR; o *= 2) {
+            const float other = __shfl_xor_sync(0xffffffffu, mean, o);
+            const float more = __shfl_xor_sync(0xffffffffu, squares, o);
+            const float d = other - mean;
+            mean = 0.5f * (mean + other);
+            squares = fmaf(d * d, 0.5f * E * o, squares + more);
+        }
+        const float r = rsqrtf(fmaf(squares, a.inv_c, a.eps));
+#pragma unroll
+        for (int i = 0; i < E; i += 2) put(z + i, __fmul2_rn(__fadd2_rn(pair(z + i), both(-mean)), both(r)));
+        return r;
+    }
     if (a.layer) {
         float2 t = make_float2(0.f, 0.f);
 #pragma unroll
@@ -131,7 +157,7 @@ __device__ __forceinline__ float normalise(float (&z)[V * VPT], const NormArgs &
     for (int i = 0; i < E; i += 2) t = __ffma2_rn(pair(z + i), pair(z + i), t);
     sum[0] = t.x + t.y;
     row_sums<TPR, 1>(sum, red, turn);
-    const float r = 1.f / sqrtf(fmaf(sum[0], a.inv_c, a.eps));
+    const float r = rsqrtf(fmaf(sum[0], a.inv_c, a.eps));  // within 2 steps of fp32
     times(z, r);
     return r;
 }
@@ -196,29 +222,34 @@ template <typename T, int TPR, int VPT, int ARRAYS, int WANTED> struct RowRing {
     static constexpr int kAhead = STAGES - 1;
     static constexpr size_t kBytes = (size_t)STAGES * kGroup;
     static_assert(kBytes <= kRoom, "one row group must fit");
-    const NormArgs &a;
-    const void *base[ARRAYS];
+    const T *src[ARRAYS];  // this thread's first vector of the next row to fetch
+    bool have[ARRAYS];
     uint8_t *mine;
-    int lane, put = 0, get = 0;
+    int64_t step;  // elements from one of the thread's rows to its next
+    int vectors;   // of the thread: those of i < VPT with lane + i TPR inside the row
+    int put = 0, get = 0;
 
-    __device__ __forceinline__ RowRing(const NormArgs &args, uint8_t *smem, int row_lane)
-        : a(args), mine(smem + threadIdx.x * 16), lane(row_lane) {}
+    __device__ __forceinline__ RowRing(const NormArgs &a, uint8_t *smem, int lane)
+        : mine(smem + threadIdx.x * 16), step((int64_t)(kThreads / TPR) * a.C), vectors((a.nvec - lane + TPR - 1) / TPR) {}
+    __device__ __forceinline__ void array(int k, const NormArgs &a, const void *base, int64_t row, int lane)
+    {
+        have[k] = base != nullptr;
+        src[k] = static_cast<const T *>(have[k] ? base : a.x) + row * a.C + (int64_t)lane * Vec16<T>::N;
+    }
     __device__ __forceinline__ uint8_t *slot(int stage, int array, int i) const
     {
         return mine + (size_t)((stage * ARRAYS + array) * VPT + i) * (kThreads * 16);
     }
-    // copies row `row` (zeros where it is not one, or an array is absent) and commits
-    __device__ __forceinline__ void fetch(int64_t row, bool in)
+    // copies the thread's next row (zeros, reading nothing, where it is not one or an array is absent) and commits
+    __device__ __forceinline__ void fetch(bool in)
     {
 #pragma unroll
-        for (int k = 0; k < ARRAYS; ++k)
+        for (int k = 0; k < ARRAYS; ++k) {
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                const bool real = in && base[k] && lane + i * TPR < a.nvec;
-                const T *src = static_cast<const T *>(real ? base[k] : a.x);
-                if (real) src += row * a.C + (int64_t)(lane + i * TPR) * Vec16<T>::N;
-                cp_async16_or_zero(smem_u32(slot(put, k, i)), src, real);
-            }
+            for (int i = 0; i < VPT; ++i)
+                cp_async16_or_zero(smem_u32(slot(put, k, i)), src[k] + i * TPR * Vec16<T>::N, in && have[k] && i < vectors);
+            src[k] += step;
+        }
         cp_async_commit();
         put = put + 1 == STAGES ? 0 : put + 1;
     }
@@ -289,10 +320,10 @@ __global__ void __launch_bounds__(block_threads(TPR), TPR > 256 ? kForwardWide :
     int turn = 0;
     grid_dependency_wait();
     Ring ring(a, reinterpret_cast<uint8_t *>(smem4), lane);
-    ring.base[0] = a.x;
-    ring.base[1] = a.h;
+    ring.array(0, a, a.x, row0 + begin + grp, lane);
+    ring.array(1, a, a.h, row0 + begin + grp, lane);
 #pragma unroll
-    for (int k = 0; k < Ring::kAhead; ++k) ring.fetch(row0 + begin + k * RPC + grp, begin + k * RPC + grp < end);
+    for (int k = 0; k < Ring::kAhead; ++k) ring.fetch(begin + k * RPC + grp < end);
     Stash<TPR, E> stash(red + 128);
     float w[kKeep ? 4 : 1][E];  // gate w_post, gate b_post, w_pre, b_pre
     if constexpr (kKeep) {
@@ -318,7 +349,7 @@ __global__ void __launch_bounds__(block_threads(TPR), TPR > 256 ? kForwardWide :
         const int64_t row = row0 + r + grp;
         const bool in = r + grp < end;
         float s[E];
-        if (Ring::kAhead == 0) ring.fetch(row, in);
+        if (Ring::kAhead == 0) ring.fetch(in);
         ring.wait();
         ring.read(0, s);
 #pragma unroll
@@ -342,7 +373,7 @@ __global__ void __launch_bounds__(block_threads(TPR), TPR > 256 ? kForwardWide :
             }
         }
         ring.next();
-        if (Ring::kAhead > 0) ring.fetch(row + Ring::kAhead * RPC, r + Ring::kAhead * RPC + grp < end);
+        if (Ring::kAhead > 0) ring.fetch(r + Ring::kAhead * RPC + grp < end);
         if (a.s && in) store_row<T, TPR, VPT>(a.s, row, a, lane, s);
         if (a.pre_w) {
             normalise<TPR, V, VPT>(s, a, lane, red, turn);
@@ -381,12 +412,12 @@ __global__ void __launch_bounds__(block_threads(TPR), TPR > 256 ? 1 : 2) norm_re
     int turn = 0;
     grid_dependency_wait();
     Ring ring(a, reinterpret_cast<uint8_t *>(smem4), lane);
-    ring.base[0] = a.x;
-    ring.base[1] = a.h;
-    ring.base[2] = a.dy;
-    ring.base[3] = a.ds;
+    ring.array(0, a, a.x, row0 + begin + grp, lane);
+    ring.array(1, a, a.h, row0 + begin + grp, lane);
+    ring.array(2, a, a.dy, row0 + begin + grp, lane);
+    ring.array(3, a, a.ds, row0 + begin + grp, lane);
 #pragma unroll
-    for (int k = 0; k < Ring::kAhead; ++k) ring.fetch(row0 + begin + k * RPC + grp, begin + k * RPC + grp < end);
+    for (int k = 0; k < Ring::kAhead; ++k) ring.fetch(begin + k * RPC + grp < end);
     float sum[SUMS][E];
 #pragma unroll
     for (int k = 0; k < SUMS; ++k)
@@ -413,7 +444,7 @@ __global__ void __launch_bounds__(block_threads(TPR), TPR > 256 ? 1 : 2) norm_re
     for (int r = begin; r < end; r += RPC) {
         const int64_t row = row0 + r + grp;
         const bool in = r + grp < end;
-        if (Ring::kAhead == 0) ring.fetch(row, in);
+        if (Ring::kAhead == 0) ring.fetch(in);
         ring.wait();
         // the forward pass again: hn = norm(h) (or h), s = alpha x + hn gw + gb
         float s[E], hn[E];
@@ -453,7 +484,7 @@ __global__ void __launch_bounds__(block_threads(TPR), TPR > 256 ? 1 : 2) norm_re
         }
         ring.read(3, s);
         ring.next();
-        if (Ring::kAhead > 0) ring.fetch(row + Ring::kAhead * RPC, r + Ring::kAhead * RPC + grp < end);
+        if (Ring::kAhead > 0) ring.fetch(r + Ring::kAhead * RPC + grp < end);
         plus(dS, s);
 #pragma unroll
         for (int i = 0; i < E; ++i) s[i] = dS[i];
