@@ -774,11 +774,14 @@ bra_status bra_diff_attend_backward(const void *q, const void *k, const void *v,
     if ((long long)g.N * topk > (1LL << 30)) return BRA_ERR_UNSUPPORTED;
     DeviceState *st = nullptr;
     if ((s = device_state(&st)) != BRA_OK) return s;
-    const bool bf16 = dtype == BRA_BF16, mma = bf16 && bra::diff_mma_supports(g);
+    const bool bf16 = dtype == BRA_BF16;
+    const bra::DiffBackward kernels = bf16 && bra::diff_backward_umma_supports(g) ? bra::DiffBackward::kUmma
+                                      : bf16 && bra::diff_mma_supports(g)         ? bra::DiffBackward::kMma
+                                                                                  : bra::DiffBackward::kSimt;
     bra::DiffArgs a = {};
     bra::diff_plan(a, g);
     const size_t stats = (size_t)B * heads * g.N * sizeof(float4);
-    const size_t parts = ((size_t)heads * bra::diff_backward_parts(g, mma) * sizeof(float) + 15) & ~(size_t)15;
+    const size_t parts = ((size_t)heads * bra::diff_backward_parts(g, kernels) * sizeof(float) + 15) & ~(size_t)15;
     const size_t list = ((size_t)B * g.R * topk * sizeof(int32_t) + 15) & ~(size_t)15;
     const size_t start = (size_t)B * (g.R + 1) * sizeof(int32_t);
     uint8_t *ws = nullptr;
@@ -803,7 +806,9 @@ bra_status bra_diff_attend_backward(const void *q, const void *k, const void *v,
     a.start = wstart;
     e = bra::launch_diff_invert(a, wlist, wstart, cs);
     if (e == cudaSuccess)
-        e = mma ? bra::launch_diff_backward_mma(a, cs) : bra::launch_diff_simt(a, true, bf16, cs);
+        e = kernels == bra::DiffBackward::kUmma  ? bra::launch_diff_backward_umma(a, cs)
+            : kernels == bra::DiffBackward::kMma ? bra::launch_diff_backward_mma(a, cs)
+                                                 : bra::launch_diff_simt(a, true, bf16, cs);
     const cudaError_t f = cudaFreeAsync(ws, cs);
     if (e != cudaSuccess) return cuda_fail(e, "differential backward kernels");
     if (f != cudaSuccess) return cuda_fail(f, "cudaFreeAsync(differential backward scratch)");

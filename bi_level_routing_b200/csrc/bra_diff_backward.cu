@@ -605,10 +605,12 @@ template <int DK> cudaError_t launch_dk(DiffArgs &a, cudaStream_t stream)
 }  // namespace
 
 // The query kernels' launches: the partial sums of D2 for each head, one for each warp's rows.
-long long diff_backward_parts(const Geometry &g, bool mma)
+long long diff_backward_parts(const Geometry &g, DiffBackward kernels)
 {
     long long per;
-    if (mma)
+    if (kernels == DiffBackward::kUmma)
+        per = 4LL * ((g.rs + 127) / 128);
+    else if (kernels == DiffBackward::kMma)
         per = g.rs <= 16 ? 1 : g.rs <= 32 ? 2 : 4LL * ((g.rs + 63) / 64);
     else
         per = g.rs <= 16 ? 4 : 8LL * ((g.rs + 63) / 64);

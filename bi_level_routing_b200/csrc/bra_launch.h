@@ -214,13 +214,16 @@ cudaError_t launch_diff_attend_tile(const DiffArgs &a, cudaStream_t stream);
 // The tcgen05 ones (bf16, the same heads): large regions.
 bool diff_umma_supports(const Geometry &g);
 cudaError_t launch_diff_attend_umma(const DiffArgs &a, cudaStream_t stream);
+bool diff_backward_umma_supports(const Geometry &g);
+cudaError_t launch_diff_backward_umma(const DiffArgs &a, cudaStream_t stream);
 cudaError_t launch_diff_attend_mma(const DiffArgs &a, cudaStream_t stream);
 cudaError_t launch_diff_backward_mma(const DiffArgs &a, cudaStream_t stream);
 cudaError_t launch_diff_simt(const DiffArgs &a, bool backward, bool bf16, cudaStream_t stream);
 // list [B, R * topk] and start [B, R + 1]: for each region the regions that route to it, in order.
 cudaError_t launch_diff_invert(const DiffArgs &a, int32_t *list, int32_t *start, cudaStream_t stream);
-// Partial sums that the backward kernels leave for each head's dlam.
-long long diff_backward_parts(const Geometry &g, bool mma);
+// Partial sums that a family of backward kernels leaves for each head's dlam.
+enum class DiffBackward { kSimt, kMma, kUmma };
+long long diff_backward_parts(const Geometry &g, DiffBackward kernels);
 
 // ---------------------------------------------------------------- rotary positions
 
