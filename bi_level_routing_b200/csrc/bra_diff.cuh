@@ -56,7 +56,7 @@ struct DiffArgs {
     int nparts;
     float scale;        // d^-1/2
     float scale_log2;   // d^-1/2 log2(e)
-    FastDiv by_rs, by_wr, by_nwin, by_heads, by_tiles, by_R;
+    FastDiv by_rs, by_wr, by_nwin, by_heads, by_tiles, by_R, by_topk;
 };
 
 // Offset y W + x (in tokens, inside an image) of token `tok` of the region whose first token lies at
@@ -130,6 +130,24 @@ __device__ __forceinline__ float finite_max(float before, float top)
 {
     const float m = fmaxf(before, top);
     return m == -INFINITY ? 0.f : m;
+}
+
+// A warp goes through ROWS rows, LANES of its lanes to a row: a lane finds the place of one row (locate(row), -1 for none,
+// some dozen instructions), the lanes that copy the row take it from there: copy(row, place).
+template <int ROWS, int LANES, typename Locate, typename Copy>
+__device__ __forceinline__ void warp_rows(int lane, Locate locate, Copy copy)
+{
+    static_assert(LANES <= 32 && 32 % LANES == 0, "whole rows to a pass");
+#pragma unroll
+    for (int r0 = 0; r0 < ROWS; r0 += 32) {
+        const int at = r0 + lane < ROWS ? locate(r0 + lane) : -1;
+#pragma unroll
+        for (int x = 0; x < (ROWS - r0 < 32 ? ROWS - r0 : 32) * LANES; x += 32) {
+            const int row = (x + lane) / LANES;
+            const int place = __shfl_sync(0xffffffffu, at, row & 31);
+            if (r0 + row < ROWS) copy(r0 + row, place);
+        }
+    }
 }
 
 // 2^x of two values on the FMA pipe, for probabilities that are rounded to bf16: x = n + f with n the

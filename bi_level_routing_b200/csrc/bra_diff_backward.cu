@@ -214,18 +214,20 @@ __global__ void __launch_bounds__(32 * kInvertWarps) diff_invert_kernel(const in
 
 // ------------------------------------------------------------------ dq, statistics
 
-template <int DK, int WPI, int KT>
-__global__ void __launch_bounds__(32 * kWarps) diff_backward_queries_kernel(const DiffArgs a)
+// SINGLE: all keys fit one tile (topk rs <= KT), whose scores stay in registers between the passes.
+template <int DK, int WPI, int KT, bool SINGLE>
+__global__ void __launch_bounds__(32 * kWarps, SINGLE && DK <= 32 ? 3 : 1) diff_backward_queries_kernel(const DiffArgs a)
 {
+    constexpr int kStages = SINGLE ? 1 : 2;
     using L = BackTile<DK>;
     constexpr int HP = L::kHp, ROW = L::kRow, NK = L::kNk, NT = KT / 8;
     extern __shared__ float4 smem4[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = warp / WPI, wg = warp % WPI, gtid = threadIdx.x % (32 * WPI);
-    const size_t group_bytes = (size_t)4 * KT * ROW * 2 + (((size_t)a.topk * 4 + 15) & ~(size_t)15) + 16;
+    const size_t group_bytes = (size_t)2 * kStages * KT * ROW * 2 + (((size_t)a.topk * 4 + 15) & ~(size_t)15) + 16;
     uint8_t *mine = reinterpret_cast<uint8_t *>(smem4) + group * group_bytes;
     __nv_bfloat16 *tiles = reinterpret_cast<__nv_bfloat16 *>(mine);  // [stage][K, V][KT][ROW]
-    int *count = reinterpret_cast<int *>(mine + (size_t)4 * KT * ROW * 2);
+    int *count = reinterpret_cast<int *>(mine + (size_t)2 * kStages * KT * ROW * 2);
     int *bases = count + 4;
     const int item = blockIdx.x * (kWarps / WPI) + group;
     if (item >= a.nitems) return;  // the whole group: its barriers are its own
@@ -237,7 +239,7 @@ __global__ void __launch_bounds__(32 * kWarps) diff_backward_queries_kernel(cons
         if (lane == 0) *count = n;
     }
     const int dc = a.d / 8;
-    if (a.d < DK) clear_padding<DK>(tiles, 4 * KT, dc, gtid, 32 * WPI);
+    if (a.d < DK) clear_padding<DK>(tiles, 2 * kStages * KT, dc, gtid, 32 * WPI);
     group_barrier<WPI>(group);
     const int nkeys = *count * a.rs;
     const int ntiles = (nkeys + KT - 1) / KT;
@@ -245,23 +247,22 @@ __global__ void __launch_bounds__(32 * kWarps) diff_backward_queries_kernel(cons
     const __nv_bfloat16 *gk = static_cast<const __nv_bfloat16 *>(a.k) + image;
     const __nv_bfloat16 *gv = static_cast<const __nv_bfloat16 *>(a.v) + image;
     auto fetch = [&](int tile, int stage) {
-        const int j = gtid % L::kLanes;
-        __nv_bfloat16 *sk = tiles + (size_t)stage * 2 * KT * ROW, *sv = sk + KT * ROW;
-        if (j < 2 * dc) {
-            const int jk = padded_chunk<DK>(j, dc);
-            for (int row = gtid / L::kLanes; row < KT; row += 32 * WPI / L::kLanes) {
-                const int key = tile * KT + row;
-                const bool real = key < nkeys;
-                int64_t off = 0;
-                if (real) {
-                    int slot, tok;
-                    a.by_rs.divmod(key, slot, tok);
-                    off = (int64_t)token_at(a, bases[slot], tok) * a.C + 8 * j;
-                }
-                cp_async16_or_zero(smem_u32(sk + row * ROW + 8 * jk), gk + off, real);
-                cp_async16_or_zero(smem_u32(sv + row * ROW + 8 * j), gv + off, real);
-            }
-        }
+        const int j = lane % L::kLanes, jk = padded_chunk<DK>(j, dc), r0 = tile * KT + wg * (KT / WPI);
+        __nv_bfloat16 *sk = tiles + (size_t)stage * 2 * KT * ROW + wg * (KT / WPI) * ROW, *sv = sk + KT * ROW;
+        warp_rows<KT / WPI, L::kLanes>(
+            lane,
+            [&](int row) {
+                if (r0 + row >= nkeys) return -1;
+                int slot, tok;
+                a.by_rs.divmod(r0 + row, slot, tok);
+                return token_at(a, bases[slot], tok);
+            },
+            [&](int row, int at) {
+                if (j >= 2 * dc) return;
+                const int64_t off = (int64_t)max(at, 0) * a.C + 8 * j;
+                cp_async16_or_zero(smem_u32(sk + row * ROW + 8 * jk), gk + off, at >= 0);
+                cp_async16_or_zero(smem_u32(sv + row * ROW + 8 * j), gv + off, at >= 0);
+            });
         cp_async_commit();
     };
     if (ntiles > 0) fetch(0, 0);
@@ -305,10 +306,11 @@ __global__ void __launch_bounds__(32 * kWarps) diff_backward_queries_kernel(cons
 
     float mx[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
     float l[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, ed[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-    for (int tile = 0; tile < ntiles; ++tile) {
+    for (int tile = 0; SINGLE ? tile < 1 : tile < ntiles; ++tile) {
         cp_async_wait_all();
         group_barrier<WPI>(group);
-        if (tile + 1 < ntiles) fetch(tile + 1, (tile + 1) & 1);
+        if (!SINGLE && tile + 1 < ntiles) fetch(tile + 1, (tile + 1) & 1);
+        if (SINGLE && ntiles == 0) break;  // no tile: nothing was fetched
         scores(tile, tile & 1);
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -362,13 +364,12 @@ __global__ void __launch_bounds__(32 * kWarps) diff_backward_queries_kernel(cons
     for (int nt = 0; nt < HP / 8; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
-    const bool single = ntiles == 1;  // its tile is still in place, its scores still in registers
-    if (ntiles > 1) {
+    if (!SINGLE && ntiles > 0) {
         group_barrier<WPI>(group);
         fetch(0, 0);
     }
-    for (int tile = 0; tile < ntiles; ++tile) {
-        if (!single) {
+    for (int tile = 0; SINGLE ? tile < (ntiles > 0) : tile < ntiles; ++tile) {
+        if (!SINGLE) {
             cp_async_wait_all();
             group_barrier<WPI>(group);
             if (tile + 1 < ntiles) fetch(tile + 1, (tile + 1) & 1);
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(32 * kWarps) diff_backward_queries_kernel(cons
 // ------------------------------------------------------------------ dk, dv, dlam
 
 template <int DK, int WPI, int QT>
-__global__ void __launch_bounds__(32 * kWarps) diff_backward_keys_kernel(const DiffArgs a)
+__global__ void __launch_bounds__(32 * kWarps, DK <= 32 ? 3 : 1) diff_backward_keys_kernel(const DiffArgs a)
 {
     using L = BackTile<DK>;
     constexpr int HP = L::kHp, ROW = L::kRow, NK = L::kNk, NT = QT / 8;
@@ -454,25 +455,23 @@ __global__ void __launch_bounds__(32 * kWarps) diff_backward_keys_kernel(const D
     const float4 *stats = a.stats + ((int64_t)it.b * a.heads + it.h) * a.N;
     if (a.d < DK) group_barrier<WPI>(group);
     auto fetch = [&](int tile, int stage) {
-        const int j = gtid % L::kLanes;
-        __nv_bfloat16 *sq = tiles + (size_t)stage * 2 * QT * ROW, *sd = sq + QT * ROW;
-        if (j < 2 * dc) {
-            const int jq = padded_chunk<DK>(j, dc);
-            for (int row = gtid / L::kLanes; row < QT; row += 32 * WPI / L::kLanes) {
-                const int query = tile * QT + row;
-                const bool real = query < nq;
-                int at = 0;
-                if (real) {
-                    int slot, tok;
-                    a.by_rs.divmod(query, slot, tok);
-                    at = token_at(a, region_at(a, __ldg(list + slot)), tok);
-                }
-                const int64_t off = (int64_t)at * a.C + 8 * j;
-                cp_async16_or_zero(smem_u32(sq + row * ROW + 8 * jq), gq + off, real);
-                cp_async16_or_zero(smem_u32(sd + row * ROW + 8 * j), gd + off, real);
-                if (j == 0) cp_async16_or_zero(smem_u32(sstat + stage * QT + row), stats + at, real);
-            }
-        }
+        const int j = lane % L::kLanes, jq = padded_chunk<DK>(j, dc), own = wg * (QT / WPI), r0 = tile * QT + own;
+        __nv_bfloat16 *sq = tiles + (size_t)stage * 2 * QT * ROW + own * ROW, *sd = sq + QT * ROW;
+        warp_rows<QT / WPI, L::kLanes>(
+            lane,
+            [&](int row) {
+                if (r0 + row >= nq) return -1;
+                int slot, tok;
+                a.by_rs.divmod(r0 + row, slot, tok);
+                return token_at(a, region_at(a, __ldg(list + slot)), tok);
+            },
+            [&](int row, int at) {
+                if (j == 0) cp_async16_or_zero(smem_u32(sstat + stage * QT + own + row), stats + max(at, 0), at >= 0);
+                if (j >= 2 * dc) return;
+                const int64_t off = (int64_t)max(at, 0) * a.C + 8 * j;
+                cp_async16_or_zero(smem_u32(sq + row * ROW + 8 * jq), gq + off, at >= 0);
+                cp_async16_or_zero(smem_u32(sd + row * ROW + 8 * j), gd + off, at >= 0);
+            });
         cp_async_commit();
     };
     if (ntiles > 0) fetch(0, 0);
@@ -576,9 +575,17 @@ template <auto Kernel> cudaError_t launch_with(int grid, size_t smem, const Diff
     return launch_pdl(Kernel, dim3(grid), dim3(32 * kWarps), smem, stream, a);
 }
 
-template <int DK, int WPI, int KT, int QT> cudaError_t launch_one(DiffArgs &a, cudaStream_t stream)
+template <int DK, int WPI, int KT, bool SINGLE> cudaError_t launch_queries(const DiffArgs &a, int grid, cudaStream_t stream)
 {
-    constexpr int ROW = BackTile<DK>::kRow, groups = kWarps / WPI;
+    constexpr int groups = kWarps / WPI;
+    return launch_with<diff_backward_queries_kernel<DK, WPI, KT, SINGLE>>(
+        grid, groups * ((size_t)(SINGLE ? 2 : 4) * KT * BackTile<DK>::kRow * 2 + round16((size_t)a.topk * 4) + 16), a, stream);
+}
+
+// Query tiles of 16 rows: the gradients' accumulators leave no more registers at three CTAs an SM.
+template <int DK, int WPI> cudaError_t launch_one(DiffArgs &a, cudaStream_t stream)
+{
+    constexpr int ROW = BackTile<DK>::kRow, groups = kWarps / WPI, QT = 16;
     a.tiles = (a.rs + 16 * WPI - 1) / (16 * WPI);
     a.by_tiles = FastDiv::of(a.tiles);
     const long long items = (long long)a.B * a.R * a.tiles * a.heads;
@@ -586,8 +593,8 @@ template <int DK, int WPI, int KT, int QT> cudaError_t launch_one(DiffArgs &a, c
     a.nitems = (int)items;
     a.nparts = (int)(items / a.heads * WPI);
     const int grid = (int)((items + groups - 1) / groups);
-    cudaError_t e = launch_with<diff_backward_queries_kernel<DK, WPI, KT>>(grid,
-                                groups * ((size_t)4 * KT * ROW * 2 + round16((size_t)a.topk * 4) + 16), a, stream);
+    const cudaError_t e = DK <= 32 && (long long)a.topk * a.rs <= 64 ? launch_queries<DK, WPI, DK <= 32 ? 64 : 32, DK <= 32>(a, grid, stream)
+                                                                     : launch_queries<DK, WPI, 32, false>(a, grid, stream);
     if (e != cudaSuccess) return e;
     constexpr size_t tile = (size_t)4 * QT * ROW * 2, keep = (size_t)16 * WPI * ROW * 2;
     return launch_with<diff_backward_keys_kernel<DK, WPI, QT>>(grid > a.heads ? grid : a.heads,
@@ -596,10 +603,9 @@ template <int DK, int WPI, int KT, int QT> cudaError_t launch_one(DiffArgs &a, c
 
 template <int DK> cudaError_t launch_dk(DiffArgs &a, cudaStream_t stream)
 {
-    constexpr int QT = DK <= 32 ? 32 : 16;
-    if (a.rs <= 16) return launch_one<DK, 1, 32, QT>(a, stream);
-    if (a.rs <= 32) return launch_one<DK, 2, 32, QT>(a, stream);
-    return launch_one<DK, 4, 32, QT>(a, stream);
+    if (a.rs <= 16) return launch_one<DK, 1>(a, stream);
+    if (a.rs <= 32) return launch_one<DK, 2>(a, stream);
+    return launch_one<DK, 4>(a, stream);
 }
 
 }  // namespace
@@ -640,6 +646,7 @@ void diff_plan(DiffArgs &a, const Geometry &g)
     a.by_nwin = FastDiv::of(g.n_win);
     a.by_heads = FastDiv::of(g.heads);
     a.by_R = FastDiv::of(g.R);
+    a.by_topk = FastDiv::of(g.topk);
 }
 
 cudaError_t launch_diff_invert(const DiffArgs &a, int32_t *list, int32_t *start, cudaStream_t stream)

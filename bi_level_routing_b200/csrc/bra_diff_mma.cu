@@ -73,23 +73,22 @@ __global__ void __launch_bounds__(32 * kWarps) diff_attend_mma_kernel(const Diff
     const __nv_bfloat16 *gk = static_cast<const __nv_bfloat16 *>(a.k) + image;
     const __nv_bfloat16 *gv = static_cast<const __nv_bfloat16 *>(a.v) + image;
     auto fetch = [&](int tile, int stage) {
-        const int j = gtid % L::kLanes;
-        __nv_bfloat16 *sk = tiles + (size_t)stage * 2 * KT * ROW, *sv = sk + KT * ROW;
-        if (j < 2 * dc) {
-            const int jk = j < dc ? j : DK / 8 + j - dc;
-            for (int row = gtid / L::kLanes; row < KT; row += 32 * WPI / L::kLanes) {
-                const int key = tile * KT + row;
-                const bool real = key < nkeys;
-                int64_t off = 0;
-                if (real) {
-                    int slot, tok;
-                    a.by_rs.divmod(key, slot, tok);
-                    off = (int64_t)token_at(a, bases[slot], tok) * a.C + 8 * j;
-                }
-                cp_async16_or_zero(smem_u32(sk + row * ROW + 8 * jk), gk + off, real);
-                cp_async16_or_zero(smem_u32(sv + row * ROW + 8 * j), gv + off, real);
-            }
-        }
+        const int j = lane % L::kLanes, jk = j < dc ? j : DK / 8 + j - dc, r0 = tile * KT + wg * (KT / WPI);
+        __nv_bfloat16 *sk = tiles + (size_t)stage * 2 * KT * ROW + wg * (KT / WPI) * ROW, *sv = sk + KT * ROW;
+        warp_rows<KT / WPI, L::kLanes>(
+            lane,
+            [&](int row) {
+                if (r0 + row >= nkeys) return -1;
+                int slot, tok;
+                a.by_rs.divmod(r0 + row, slot, tok);
+                return token_at(a, bases[slot], tok);
+            },
+            [&](int row, int at) {
+                if (j >= 2 * dc) return;
+                const int64_t off = (int64_t)max(at, 0) * a.C + 8 * j;
+                cp_async16_or_zero(smem_u32(sk + row * ROW + 8 * jk), gk + off, at >= 0);
+                cp_async16_or_zero(smem_u32(sv + row * ROW + 8 * j), gv + off, at >= 0);
+            });
         cp_async_commit();
     };
     if (ntiles > 0) fetch(0, 0);

@@ -89,25 +89,22 @@ __global__ void __launch_bounds__(32 * kWarps, DK <= 32 ? 4 : 3) diff_attend_til
         nkeys = *count * a.rs;
     }
     {
-        const int j = gtid % L::kLanes;
-        if (j < 2 * dc) {
-            const int jk = j < dc ? j : DK / 8 + j - dc;
-            for (int row = gtid / L::kLanes; row < KT; row += 32 * WPI / L::kLanes) {
-                const bool real = row < nkeys;
-                int64_t off = 0;
-                if (real) {
-                    if (DENSE) {
-                        off = (int64_t)row * a.C + 8 * j;
-                    } else {
-                        int slot, tok;
-                        a.by_rs.divmod(row, slot, tok);
-                        off = (int64_t)token_at(a, bases[slot], tok) * a.C + 8 * j;
-                    }
-                }
-                cp_async16_or_zero(smem_u32(sk + row * ROW + 8 * jk), gk + off, real);
-                cp_async16_or_zero(smem_u32(sv + row * ROW + 8 * j), gv + off, real);
-            }
-        }
+        const int j = lane % L::kLanes, jk = j < dc ? j : DK / 8 + j - dc, r0 = wg * (KT / WPI);
+        warp_rows<KT / WPI, L::kLanes>(
+            lane,
+            [&](int row) {
+                if (r0 + row >= nkeys) return -1;
+                if (DENSE) return r0 + row;
+                int slot, tok;
+                a.by_rs.divmod(r0 + row, slot, tok);
+                return token_at(a, bases[slot], tok);
+            },
+            [&](int row, int at) {
+                if (j >= 2 * dc) return;
+                const int64_t off = (int64_t)max(at, 0) * a.C + 8 * j;
+                cp_async16_or_zero(smem_u32(sk + (r0 + row) * ROW + 8 * jk), gk + off, at >= 0);
+                cp_async16_or_zero(smem_u32(sv + (r0 + row) * ROW + 8 * j), gv + off, at >= 0);
+            });
         cp_async_commit();
     }
     // the warp's query rows g and g + 8, both maps, as A fragments straight from global memory
@@ -136,18 +133,29 @@ __global__ void __launch_bounds__(32 * kWarps, DK <= 32 ? 4 : 3) diff_attend_til
     if (DENSE) {
         group_barrier<WPI>(group);  // the counts are cleared
         const int32_t *row = a.idx + (int64_t)it.b * a.R * a.topk;
-        for (int e = gtid; e < a.R * a.topk; e += 32 * WPI) {
-            const int s = __ldg(row + e);
-            if (s < 0 || s >= a.R) {
-                flag_error(a.err, kErrIndex);
-                continue;
+        constexpr int kAhead = 8;  // index entries in flight for each thread
+        for (int e0 = gtid; e0 < a.R * a.topk; e0 += kAhead * 32 * WPI) {
+            int named[kAhead];
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) {
+                const int e = e0 + x * 32 * WPI;
+                named[x] = e < a.R * a.topk ? __ldg(row + e) : 0;
             }
-            const int from = region_at(a, e / a.topk), to = region_at(a, s);
-            for (int x = 0; x < a.rs; ++x) {
-                const int query = token_at(a, from, x);
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) {
+                const int e = e0 + x * 32 * WPI, s = named[x];
+                if (e >= a.R * a.topk) break;
+                if (s < 0 || s >= a.R) {
+                    flag_error(a.err, kErrIndex);
+                    continue;
+                }
+                const int from = region_at(a, a.by_topk.div(e)), to = region_at(a, s);
                 for (int y = 0; y < a.rs; ++y) {
-                    const int key = token_at(a, to, y);
-                    atomicAdd(pairs + query * 16 + (key >> 2), 1u << (8 * (key & 3)));  // at most topk <= 64 of each
+                    const int query = token_at(a, from, y);
+                    for (int z = 0; z < a.rs; ++z) {
+                        const int key = token_at(a, to, z);
+                        atomicAdd(pairs + query * 16 + (key >> 2), 1u << (8 * (key & 3)));  // at most topk <= 64 of each
+                    }
                 }
             }
         }
