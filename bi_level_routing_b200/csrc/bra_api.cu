@@ -688,6 +688,16 @@ bra_status bra_attend_backward(const void *q, const void *k, const void *v, cons
 
 // ---------------------------------------------------------------- differential attention
 
+// Whether [p, p + bytes) and [r, r + bytes) share memory without being the same buffer.
+static bool overlaps(const void *p, const void *r, size_t bytes)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(r);
+    return x != y && (x < y ? y - x : x - y) < bytes;
+}
+
+// Whether two buffers of `bytes` share memory at all.
+static bool shares(const void *p, const void *r, size_t bytes) { return p == r || overlaps(p, r, bytes); }
+
 // The sizes both passes take: heads of a multiple of 8 channels, at most 128.
 static bra_status check_diff(int B, int H, int W, int C, int heads, int n_win, int topk, bra_dtype dtype, bool routes,
                              bra::Geometry *g)
@@ -730,6 +740,8 @@ bra_status bra_diff_attend(const void *q, const void *k, const void *v, const in
     if (B == 0) return BRA_OK;
     if ((s = check_data_ptrs(q, k, v, idx, out)) != BRA_OK) return s;
     if (!lambda || !aligned(lambda, 4)) return BRA_ERR_INVALID_ARG;
+    const size_t bytes = (size_t)B * H * W * C * (dtype == BRA_BF16 ? 2 : 4);
+    if (shares(out, q, bytes) || shares(out, k, bytes) || shares(out, v, bytes)) return BRA_ERR_INVALID_ARG;
     return diff_attend_impl(q, k, v, idx, lambda, out, g, dtype, static_cast<cudaStream_t>(stream));
 }
 
@@ -742,13 +754,14 @@ bra_status bra_forward_diff(const void *q, const void *k, const void *v, int32_t
     if (B == 0) return BRA_OK;
     if ((s = check_data_ptrs(q, k, v, idx, out)) != BRA_OK) return s;
     if (!lambda || !aligned(lambda, 4)) return BRA_ERR_INVALID_ARG;
+    const size_t bytes = (size_t)B * H * W * C * (dtype == BRA_BF16 ? 2 : 4);
+    if (shares(out, q, bytes) || shares(out, k, bytes) || shares(out, v, bytes)) return BRA_ERR_INVALID_ARG;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (g.R == 1) {  // one region routes to itself whatever its affinity
         const cudaError_t e = cudaMemsetAsync(idx, 0, (size_t)B * sizeof(int32_t), cs);
         if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(idx)");
     } else {
-        const size_t out_bytes = (size_t)B * H * W * C * (dtype == BRA_BF16 ? 2 : 4);
-        if ((s = route_impl(q, k, idx, g, dtype, cs, out, out_bytes)) != BRA_OK) return s;
+        if ((s = route_impl(q, k, idx, g, dtype, cs, out, bytes)) != BRA_OK) return s;
     }
     return diff_attend_impl(q, k, v, idx, lambda, out, g, dtype, cs);
 }
@@ -770,6 +783,13 @@ bra_status bra_diff_attend_backward(const void *q, const void *k, const void *v,
     if (!lambda || !dq || !dk || !dv || !dlambda || !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) ||
         !aligned(lambda, 4) || !aligned(dlambda, 4))
         return BRA_ERR_INVALID_ARG;
+    const size_t bytes = (size_t)B * H * W * C * (dtype == BRA_BF16 ? 2 : 4);
+    const void *const ins[] = {q, k, v, dout}, *const outs[] = {dq, dk, dv};
+    for (int i = 0; i < 3; ++i) {
+        for (const void *in : ins)
+            if (shares(outs[i], in, bytes)) return BRA_ERR_INVALID_ARG;
+        if (shares(outs[i], outs[(i + 1) % 3], bytes)) return BRA_ERR_INVALID_ARG;
+    }
     // the queries that meet one region are numbered in 31 bits
     if ((long long)g.N * topk > (1LL << 30)) return BRA_ERR_UNSUPPORTED;
     DeviceState *st = nullptr;
@@ -816,13 +836,6 @@ bra_status bra_diff_attend_backward(const void *q, const void *k, const void *v,
 }
 
 // ---------------------------------------------------------------- rotary positions
-
-// Whether [p, p + bytes) and [r, r + bytes) share memory without being the same buffer.
-static bool overlaps(const void *p, const void *r, size_t bytes)
-{
-    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(r);
-    return x != y && (x < y ? y - x : x - y) < bytes;
-}
 
 bra_status bra_rope(const void *q, const void *k, void *q_out, void *k_out, const float *freqs, const int32_t *positions,
                     int64_t y0, int64_t x0, int B, int H, int W, int C, int heads, int n, int axes, int interleaved,

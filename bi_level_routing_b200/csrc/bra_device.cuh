@@ -390,6 +390,14 @@ __device__ __forceinline__ float fmax3(float a, float b, float c)
     return d;
 }
 
+// The same, NaN if any of the three is.
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // Named barrier among `threads` threads (a multiple of 32) with id `id` (1..15).
 __device__ __forceinline__ void named_barrier(int id, int threads)
 {

@@ -153,7 +153,7 @@ __device__ __forceinline__ void warp_rows(int lane, Locate locate, Copy copy)
 // 2^x of two values on the FMA pipe, for probabilities that are rounded to bf16: x = n + f with n the
 // nearest integer (added to 1.5 2^23, where a float's last bit counts ones), 2^f a cubic fitted to least
 // relative error on [-1/2, 1/2] (7.5e-5, a 26th of a bf16 rounding), n added to its exponent. x below
-// -126 counts as -126. NaN gives a finite value: callers' rows hold NaN in their maximum or other pairs.
+// -126 counts as -126. A NaN or +inf x gives some finite value: the caller looks for them in the row's maximum.
 __device__ __forceinline__ float2 poly_exp2(float2 x)
 {
     const float2 magic = make_float2(12582912.f, 12582912.f), back = make_float2(-12582912.f, -12582912.f);
@@ -203,6 +203,15 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
         "r"(a_tmem), "r"(b_low), "r"(idesc), "r"((uint32_t)add), "r"(kDescHigh)
         : "memory");
+}
+
+// x / sum of a row's probabilities, and the row's max + log2(sum) (so that P = 2^(scale S - that)). A row without keys
+// (some = false) has weights 0 and a log of +inf. A row with keys whose sum is not positive held a NaN or +inf score (NaN
+// sum) or only -inf ones (sum 0): its softmax is NaN.
+__device__ __forceinline__ float over_sum(float x, float sum, bool some) { return sum > 0.f ? x / sum : some ? NAN : 0.f; }
+__device__ __forceinline__ float log_sum(float max, float sum, bool some)
+{
+    return sum > 0.f ? max + log2f(sum) : some ? NAN : INFINITY;
 }
 
 __device__ __forceinline__ float quad_max(float x)

@@ -328,6 +328,7 @@ __global__ void __launch_bounds__(32 * kWarps, SINGLE && DK <= 32 ? 3 : 1) diff_
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const float e = fast_exp2(fmaf(s[m][nt][2 * hh + i], a.scale_log2, -mn));
+                        if (SINGLE) s[m][nt][2 * hh + i] = e;
                         es += e;
                         eds = fmaf(e, dp[nt][2 * hh + i], eds);
                     }
@@ -342,8 +343,9 @@ __global__ void __launch_bounds__(32 * kWarps, SINGLE && DK <= 32 ? 3 : 1) diff_
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
             const float sum = quad_sum(l[m][hh]), num = quad_sum(ed[m][hh]);
-            Ls[m][hh] = sum > 0.f ? mx[m][hh] + log2f(sum) : INFINITY;
-            D[m][hh] = sum > 0.f ? num / sum : 0.f;
+            Ls[m][hh] = log_sum(mx[m][hh], sum, nkeys > 0);
+            D[m][hh] = over_sum(num, sum, nkeys > 0);
+            l[m][hh] = over_sum(1.f, sum, nkeys > 0);
         }
     float dsum = 0.f;
     float4 *stats = a.stats + ((int64_t)it.b * a.heads + it.h) * a.N;
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(32 * kWarps, SINGLE && DK <= 32 ? 3 : 1) diff_
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float p = fast_exp2(fmaf(s[m][nt][i], a.scale_log2, -Ls[m][i >> 1]));
+                    const float p = SINGLE ? s[m][nt][i] * l[m][i >> 1] : fast_exp2(fmaf(s[m][nt][i], a.scale_log2, -Ls[m][i >> 1]));
                     s[m][nt][i] = p * (dp[nt][i] - D[m][i >> 1]);
                 }
             uint32_t pf[KT / 16][4];
@@ -619,7 +621,7 @@ long long diff_backward_parts(const Geometry &g, DiffBackward kernels)
     else if (kernels == DiffBackward::kMma)
         per = g.rs <= 16 ? 1 : g.rs <= 32 ? 2 : 4LL * ((g.rs + 63) / 64);
     else
-        per = g.rs <= 16 ? 4 : 8LL * ((g.rs + 63) / 64);
+        per = g.rs <= 16 ? 4 : 4LL * ((g.rs + 31) / 32);
     return (long long)g.B * g.R * per;
 }
 

@@ -346,8 +346,8 @@ template <int NB> __global__ void __launch_bounds__(kThreads, 1) diff_backward_q
             const float top = finite_max(x[0], y[0]);
             const float wx = fast_exp2(x[0] - top), wy = fast_exp2(y[0] - top);
             const float sum = x[256] * wx + y[256] * wy, num = x[512] * wx + y[512] * wy;
-            Ls[m] = sum > 0.f ? top + log2f(sum) : INFINITY;  // a query without keys takes part in nothing
-            D[m] = sum > 0.f ? num / sum : 0.f;
+            Ls[m] = log_sum(top, sum, nkeys > 0);
+            D[m] = over_sum(num, sum, nkeys > 0);
         }
         const bool in = tok0 + row < a.rs;
         const int token = in ? token_at(a, region, tok0 + row) : 0;

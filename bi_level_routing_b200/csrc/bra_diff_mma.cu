@@ -219,8 +219,7 @@ __global__ void __launch_bounds__(32 * kWarps) diff_attend_mma_kernel(const Diff
     __nv_bfloat16 *rows = tiles + (size_t)wg * 16 * ROW;
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
-        const float l1 = quad_sum(l[0][hh]), l2 = quad_sum(l[1][hh]);
-        const float w1 = l1 > 0.f ? 1.f / l1 : 0.f, w2 = l2 > 0.f ? -lam / l2 : 0.f;
+        const float w1 = over_sum(1.f, quad_sum(l[0][hh]), nkeys > 0), w2 = over_sum(-lam, quad_sum(l[1][hh]), nkeys > 0);
 #pragma unroll
         for (int nt = 0; nt < HP / 8; ++nt) {
             const float x = fmaf(o[0][nt][2 * hh], w1, o[1][nt][2 * hh] * w2);

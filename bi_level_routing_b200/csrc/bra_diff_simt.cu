@@ -43,26 +43,35 @@ __device__ __forceinline__ void stage_vector(float *tile, int hd, int row, int u
     for (int i = 0; i < V / 4; ++i) dst[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
 }
 
-// acc[i][0..1] += rows[i] . tile[lane], tile[lane + 32] over channels [c0, c1)
+// acc[i][0..1] += rows[i] . tile[lane], tile[lane + 32] over channels [c0, c1); packed over pairs of channels
 template <int RW>
 __device__ __forceinline__ void lane_products(float (&acc)[RW][2], const float *rows, const float *tile, int hd, int lane,
                                               int c0, int c1)
 {
     const float *t0 = tile + lane * (hd + 4), *t1 = t0 + 32 * (hd + 4);
+    float2 s[RW][2];
+#pragma unroll
+    for (int i = 0; i < RW; ++i) s[i][0] = s[i][1] = make_float2(0.f, 0.f);
 #pragma unroll 1
     for (int c = c0; c < c1; c += 4) {
         const float4 x = *reinterpret_cast<const float4 *>(t0 + c), y = *reinterpret_cast<const float4 *>(t1 + c);
 #pragma unroll
         for (int i = 0; i < RW; ++i) {
             const float4 q = *reinterpret_cast<const float4 *>(rows + i * (hd + 4) + c);
-            acc[i][0] = fmaf(q.x, x.x, fmaf(q.y, x.y, fmaf(q.z, x.z, fmaf(q.w, x.w, acc[i][0]))));
-            acc[i][1] = fmaf(q.x, y.x, fmaf(q.y, y.y, fmaf(q.z, y.z, fmaf(q.w, y.w, acc[i][1]))));
+            const float2 lo = make_float2(q.x, q.y), hi = make_float2(q.z, q.w);
+            s[i][0] = __ffma2_rn(lo, make_float2(x.x, x.y), __ffma2_rn(hi, make_float2(x.z, x.w), s[i][0]));
+            s[i][1] = __ffma2_rn(lo, make_float2(y.x, y.y), __ffma2_rn(hi, make_float2(y.z, y.w), s[i][1]));
         }
+    }
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+        acc[i][0] += s[i][0].x + s[i][0].y;
+        acc[i][1] += s[i][1].x + s[i][1].y;
     }
 }
 
-// o[i][cc] += sum over the tile's rows j of p[i][j] tile[j][lane + 32 cc]; p of channel c is pa for
-// c < split, else pb
+// o[i][cc] += sum over the tile's rows j of p[i][j] tile[j][lane + 32 cc], packed over pairs of rows; p of channel c is pa
+// for c < split, else pb
 template <int RW, int NC>
 __device__ __forceinline__ void turn_products(float (&o)[RW][NC], const float *pa, const float *pb, int split,
                                               const float *tile, int hd, int lane)
@@ -71,16 +80,21 @@ __device__ __forceinline__ void turn_products(float (&o)[RW][NC], const float *p
     for (int cc = 0; cc < NC; ++cc) {
         const int c = min(lane + 32 * cc, hd - 1);
         const float *p = c < split ? pa : pb;
+        float2 s[RW];
+#pragma unroll
+        for (int i = 0; i < RW; ++i) s[i] = make_float2(0.f, 0.f);
 #pragma unroll 1
         for (int j = 0; j < kTileRows; j += 4) {
-            const float v0 = tile[j * (hd + 4) + c], v1 = tile[(j + 1) * (hd + 4) + c];
-            const float v2 = tile[(j + 2) * (hd + 4) + c], v3 = tile[(j + 3) * (hd + 4) + c];
+            const float2 v0 = make_float2(tile[j * (hd + 4) + c], tile[(j + 1) * (hd + 4) + c]);
+            const float2 v1 = make_float2(tile[(j + 2) * (hd + 4) + c], tile[(j + 3) * (hd + 4) + c]);
 #pragma unroll
             for (int i = 0; i < RW; ++i) {
                 const float4 w = *reinterpret_cast<const float4 *>(p + i * kTileRows + j);
-                o[i][cc] = fmaf(w.x, v0, fmaf(w.y, v1, fmaf(w.z, v2, fmaf(w.w, v3, o[i][cc]))));
+                s[i] = __ffma2_rn(make_float2(w.x, w.y), v0, __ffma2_rn(make_float2(w.z, w.w), v1, s[i]));
             }
         }
+#pragma unroll
+        for (int i = 0; i < RW; ++i) o[i][cc] += s[i].x + s[i].y;
     }
 }
 
@@ -162,9 +176,9 @@ __global__ void __launch_bounds__(32 * WARPS) diff_attend_simt_kernel(const Diff
                 for (int x = 0; x < 2; ++x)
                     if (k0 + lane + 32 * x >= nkeys) s[i][x] = -INFINITY;
                 const float mn = finite_max(mx[m][i], warp_max(fmaxf(s[i][0], s[i][1])) * a.scale_log2);
-                const float corr = exp2f(mx[m][i] - mn);
+                const float corr = fast_exp2(mx[m][i] - mn);
                 mx[m][i] = mn;
-                const float e0 = exp2f(fmaf(s[i][0], a.scale_log2, -mn)), e1 = exp2f(fmaf(s[i][1], a.scale_log2, -mn));
+                const float e0 = fast_exp2(fmaf(s[i][0], a.scale_log2, -mn)), e1 = fast_exp2(fmaf(s[i][1], a.scale_log2, -mn));
                 l[m][i] = l[m][i] * corr + (e0 + e1);
                 sp[(m * RW + i) * kTileRows + lane] = e0;
                 sp[(m * RW + i) * kTileRows + lane + 32] = e1;
@@ -185,8 +199,7 @@ __global__ void __launch_bounds__(32 * WARPS) diff_attend_simt_kernel(const Diff
     for (int i = 0; i < RW; ++i) {
         const int tok = it.t * ROWS + warp * RW + i;
         if (tok >= a.rs) break;
-        const float l1 = warp_sum(l[0][i]), l2 = warp_sum(l[1][i]);
-        const float w1 = l1 > 0.f ? 1.f / l1 : 0.f, w2 = l2 > 0.f ? -lam / l2 : 0.f;
+        const float w1 = over_sum(1.f, warp_sum(l[0][i]), nkeys > 0), w2 = over_sum(-lam, warp_sum(l[1][i]), nkeys > 0);
         T *dst = out + (int64_t)token_at(a, region, tok) * a.C;
 #pragma unroll
         for (int cc = 0; cc < NC; ++cc) {
@@ -272,9 +285,9 @@ __global__ void __launch_bounds__(32 * WARPS) diff_backward_queries_simt_kernel(
                 for (int x = 0; x < 2; ++x)
                     if (k0 + lane + 32 * x >= nkeys) s[i][x] = -INFINITY;
                 const float mn = finite_max(mx[m][i], warp_max(fmaxf(s[i][0], s[i][1])) * a.scale_log2);
-                const float corr = exp2f(mx[m][i] - mn);
+                const float corr = fast_exp2(mx[m][i] - mn);
                 mx[m][i] = mn;
-                const float e0 = exp2f(fmaf(s[i][0], a.scale_log2, -mn)), e1 = exp2f(fmaf(s[i][1], a.scale_log2, -mn));
+                const float e0 = fast_exp2(fmaf(s[i][0], a.scale_log2, -mn)), e1 = fast_exp2(fmaf(s[i][1], a.scale_log2, -mn));
                 l[m][i] = l[m][i] * corr + (e0 + e1);
                 ed[m][i] = ed[m][i] * corr + fmaf(e0, dp[i][0], e1 * dp[i][1]);
             }
@@ -287,8 +300,8 @@ __global__ void __launch_bounds__(32 * WARPS) diff_backward_queries_simt_kernel(
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             const float sum = warp_sum(l[m][i]), num = warp_sum(ed[m][i]);
-            Ls[m][i] = sum > 0.f ? mx[m][i] + log2f(sum) : INFINITY;
-            D[m][i] = sum > 0.f ? num / sum : 0.f;
+            Ls[m][i] = log_sum(mx[m][i], sum, nkeys > 0);
+            D[m][i] = over_sum(num, sum, nkeys > 0);
         }
         const int tok = it.t * ROWS + warp * RW + i;
         if (tok < a.rs) {
@@ -320,7 +333,7 @@ __global__ void __launch_bounds__(32 * WARPS) diff_backward_queries_simt_kernel(
             for (int i = 0; i < RW; ++i)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const float p = exp2f(fmaf(s[i][x], a.scale_log2, -Ls[m][i]));
+                    const float p = fast_exp2(fmaf(s[i][x], a.scale_log2, -Ls[m][i]));
                     sp[(m * RW + i) * kTileRows + lane + 32 * x] =
                         k0 + lane + 32 * x < nkeys ? p * (dp[i][x] - D[m][i]) : 0.f;
                 }
@@ -429,8 +442,8 @@ __global__ void __launch_bounds__(32 * WARPS) diff_backward_keys_simt_kernel(con
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const bool real = q0 + lane + 32 * x < nq;
-                const float p1 = exp2f(fmaf(s1[i][x], a.scale_log2, -st[x].x));
-                const float p2 = exp2f(fmaf(s2[i][x], a.scale_log2, -st[x].y));
+                const float p1 = fast_exp2(fmaf(s1[i][x], a.scale_log2, -st[x].x));
+                const float p2 = fast_exp2(fmaf(s2[i][x], a.scale_log2, -st[x].y));
                 float *dst = sp + i * kTileRows + lane + 32 * x;
                 dst[0] = real ? fmaf(-lam, p2, p1) : 0.f;
                 dst[RW * kTileRows] = real ? p1 * (dp[i][x] - st[x].z) : 0.f;
@@ -494,7 +507,7 @@ template <typename T, int NC> cudaError_t launch_nc(DiffArgs &a, bool backward, 
 {
     if (a.rs <= 4) return launch_one<T, 4, 1, NC>(a, backward, stream);
     if (a.rs <= 16) return launch_one<T, 4, 4, NC>(a, backward, stream);
-    return launch_one<T, 8, 8, NC>(a, backward, stream);
+    return launch_one<T, 4, 8, NC>(a, backward, stream);
 }
 
 template <typename T> cudaError_t launch_t(DiffArgs &a, bool backward, cudaStream_t stream)

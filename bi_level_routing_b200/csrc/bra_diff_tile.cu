@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(32 * kWarps, DK <= 32 ? 4 : 3) diff_attend_til
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
         float w[2];
+        bool keys = false;  // the row has any
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             float top = -INFINITY;
@@ -224,6 +225,7 @@ __global__ void __launch_bounds__(32 * kWarps, DK <= 32 ? 4 : 3) diff_attend_til
             for (int nt = 0; nt < NT; ++nt) top = fmax3(top, s[m][nt][2 * hh], s[m][nt][2 * hh + 1]);
             const float mx = finite_max(-INFINITY, quad_max(top) * a.scale_log2);
             float sum = 0.f;
+            uint32_t some = 0;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 uint32_t named = 0;
@@ -232,19 +234,23 @@ __global__ void __launch_bounds__(32 * kWarps, DK <= 32 ? 4 : 3) diff_attend_til
                 for (int i = 0; i < 2; ++i) {
                     float e = fast_exp2(fmaf(s[m][nt][2 * hh + i], a.scale_log2, -mx));
                     if (DENSE) e *= (float)((named >> (8 * i)) & 255u);
+                    if (DENSE && m == 0) some |= named;
                     s[m][nt][2 * hh + i] = e;
                     sum += e;
                 }
             }
-            sum = quad_sum(sum);
-            w[m] = sum > 0.f ? 1.f / sum : 0.f;
+            if (m == 0) {
+                some |= __shfl_xor_sync(0xffffffffu, some, 1);
+                some |= __shfl_xor_sync(0xffffffffu, some, 2);
+                keys = DENSE ? some != 0u : nkeys > 0;
+            }
+            w[m] = over_sum(m ? -lam : 1.f, quad_sum(sum), keys);
         }
-        const float w2 = w[1] > 0.f ? -lam * w[1] : 0.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                s[0][nt][2 * hh + i] = fmaf(s[0][nt][2 * hh + i], w[0], s[1][nt][2 * hh + i] * w2);
+                s[0][nt][2 * hh + i] = fmaf(s[0][nt][2 * hh + i], w[0], s[1][nt][2 * hh + i] * w[1]);
     }
     uint32_t p[KT / 16][4];
 #pragma unroll

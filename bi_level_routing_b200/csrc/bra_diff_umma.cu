@@ -283,11 +283,11 @@ __global__ void __launch_bounds__(kThreads, KT == 32 ? 2 : 1) diff_attend_umma_k
                     const float s0 = __uint_as_float(v[x / 16][(2 * x) % 32]), s1 = __uint_as_float(v[x / 16][(2 * x) % 32 + 1]);
                     const float2 e = __ffma2_rn(make_float2(s0, s1), sc, nm);
                     const float2 p = x * kUnitPairs % 32 < kUnitPairs ? make_float2(fast_exp2(e.x), fast_exp2(e.y)) : poly_exp2(e);
-                    top[x & 3] = fmax3(top[x & 3], s0, s1);
+                    top[x & 3] = fmax3_nan(top[x & 3], s0, s1);
                     ls[x & 1] = __fadd2_rn(ls[x & 1], p);
                     pw[x] = pack_bf16x2(p.x, p.y);
                 }
-                t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+                t = fmax3_nan(fmax3_nan(top[0], top[1], top[2]), top[3], top[3]) * a.scale_log2;
             };
             probabilities(mx == -INFINITY ? 0.f : -mx);
             const bool grown = t > mx + kGrowth || (mx == -INFINITY && t != -INFINITY);
@@ -319,19 +319,19 @@ __global__ void __launch_bounds__(kThreads, KT == 32 ? 2 : 1) diff_attend_umma_k
                 tmem_st_32x16(t_s, pw);
             tmem_wait_st();
             const float2 add = __fadd2_rn(ls[0], ls[1]);
-            l += add.x + add.y;
+            l += t < INFINITY ? add.x + add.y : NAN;  // a NaN or +inf score makes its row NaN
             tcgen05_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[2 * m + (i & 1)]);
         }
         // out = O1 / l1 - lam O2 / l2: thread `row` of map m's warps writes half m of the row's channels
-        sum[128 * m + row] = l;
+        sum[128 * m + row] = mx == -INFINITY ? 0.f : l;  // only -inf scores: the polynomial's least values are not a sum
         named_barrier(1, 256);
         for (int x = 0; x < 2 && ntiles > 0 && alive; ++x)  // the commit after the last tile's products
             alive = mbar_wait(&s_full[2 * x + ((ntiles + 1) & 1)], (uint32_t)(((ntiles + 1) >> 1) & 1), a.err);
         tcgen05_after_sync();
         const float l1 = sum[row], l2 = sum[128 + row], lam = __ldg(a.lam + it.h);
-        const float w1 = l1 > 0.f ? 1.f / l1 : 0.f, w2 = l2 > 0.f ? -lam / l2 : 0.f;
+        const float w1 = over_sum(1.f, l1, nkeys > 0), w2 = over_sum(-lam, l2, nkeys > 0);
         const bool in = tok0 + row < a.rs;
         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + image + 32 * NB * m;
         if (in) out += (int64_t)token_at(a, region, tok0 + row) * a.C;

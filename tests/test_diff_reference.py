@@ -102,20 +102,28 @@ def test_diff_rejects_sizes(L, kw, status):
 
 
 def test_diff_rejects_pointers(L):
-    for n, fn in ((6, L.bra_diff_attend), (6, L.bra_forward_diff), (10, L.bra_diff_attend_backward)):
+    apart = [P + (i << 24) for i in range(10)]  # buffers that share nothing
+    for n, outs, fn in ((6, (5,), L.bra_diff_attend), (6, (5,), L.bra_forward_diff), (10, (6, 7, 8), L.bra_diff_attend_backward)):
         for i in range(n):
             for bad in (0, P + 2):
-                p = [P] * n
+                p = apart[:n]
                 p[i] = bad
                 assert fn(*p, *_sizes({}), None) == INVALID, (fn.__name__, i, bad)
+        for i in outs:  # an output over an input, or a part of it
+            for j in (0, 1, 2):
+                for shift in (0, 64):
+                    p = apart[:n]
+                    p[i] = p[j] + shift
+                    assert fn(*p, *_sizes({}), None) == INVALID, (fn.__name__, i, j)
         if fn is not L.bra_diff_attend_backward:
             assert fn(*[0] * n, *_sizes(dict(B=0)), None) == OK
     # the routing limit on a region's row segment does not hold where nothing is routed
     wide = _sizes(dict(H=7, W=7 * 600, C=64, heads=1))
-    assert L.bra_forward_diff(P, P, P, P, P, P, *wide, None) == UNSUPPORTED
+    assert L.bra_forward_diff(*apart[:6], *wide, None) == UNSUPPORTED
     # more (token, slot) pairs than the backward pass numbers
     many = _sizes(dict(H=1 << 12, W=1 << 12, C=8, heads=1, n_win=16, topk=256))
-    assert L.bra_diff_attend_backward(*[P] * 10, *many, None) == UNSUPPORTED
+    far = [P + (i << 40) for i in range(10)]
+    assert L.bra_diff_attend_backward(*far, *many, None) == UNSUPPORTED
 
 
 def test_rope_rejects(L):

@@ -115,6 +115,30 @@ def test_not_finite_outside_the_routed_regions(dtype, rs):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(1, 1, 1, 7, 5, 1, 64), (1, 4, 4, 3, 2, 1, 64), (1, 3, 4, 3, 7, 1, 32), (1, 9, 9, 2, 2, 1, 64), (1, 16, 15, 1, 1, 1, 128)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_not_finite_scores_make_their_rows_nan(shape, dtype):
+    """A NaN or infinite element of a query or a key: outputs and gradients are not finite exactly where the 64-bit
+    definition's are (a query's own row; every query that names the key's region), and elsewhere what they were."""
+    B, hr, wr, n_win, topk, heads, hd = shape
+    for where, bad in (("q", "nan"), ("k", "nan"), ("k", "inf"), ("q", "-inf")):
+        q, k, v, idx, lam, dout = make(*shape, dtype, 50)
+        idx[0, 0] = n_win * n_win - 1
+        t = {"q": q, "k": k}[where]
+        t.view(-1, hd)[-1 if where == "k" else 0, 3] = float(bad)
+        want = ref.diff(q, k, v, idx, lam, heads, n_win, dout)
+        out = bra.diff_attend(q, k, v, idx, lam, heads, n_win)
+        dq, dk, dv, _ = bra.diff_attend_backward(q, k, v, idx, lam, dout, heads, n_win)
+        for name, got in (("out", out), ("dq", dq), ("dk", dk), ("dv", dv)):
+            finite = torch.isfinite(want[name])
+            assert 0 < int((~finite).sum()), (where, bad, name)
+            assert torch.equal(torch.isfinite(got.cpu()), finite), (where, bad, name, int((torch.isfinite(got.cpu()) != finite).sum()))
+            ok = finite & torch.isfinite(want[name + "_tol"])
+            if bool(ok.any()):
+                ref.check(got.cpu()[ok], want[name][ok], want[name + "_tol"][ok], f"{where} {bad} {name}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 def test_not_finite_values_reach_their_own_queries(dtype):
     """One infinite value: the queries whose rows name its region get an infinity or NaN in that channel,
     all others and all other channels what they had."""
