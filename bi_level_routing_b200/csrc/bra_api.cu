@@ -716,6 +716,7 @@ static bra_status diff_attend_impl(const void *q, const void *k, const void *v, 
     if (s != BRA_OK) return s;
     bra::DiffArgs a = {};
     bra::diff_plan(a, g);
+    a.num_sms = st->num_sms;
     a.q = q;
     a.k = k;
     a.v = v;

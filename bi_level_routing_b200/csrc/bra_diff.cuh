@@ -54,6 +54,7 @@ struct DiffArgs {
     int tiles;      // tiles of a region's tokens
     int nitems;     // work items of the launch
     int nparts;
+    int num_sms;
     float scale;        // d^-1/2
     float scale_log2;   // d^-1/2 log2(e)
     FastDiv by_rs, by_wr, by_nwin, by_heads, by_tiles, by_R, by_topk;

@@ -44,6 +44,8 @@ SHAPES = [
     (2, 2, 2, 7, 16, 2, 64), (1, 5, 3, 3, 2, 2, 48), (2, 4, 4, 7, 4, 2, 64), (1, 17, 1, 2, 3, 1, 64), (1, 4, 5, 3, 5, 2, 32),
     (2, 8, 4, 2, 2, 1, 128), (1, 3, 11, 2, 4, 2, 64), (2, 8, 8, 3, 1, 1, 64), (1, 9, 7, 2, 3, 2, 80), (1, 10, 10, 2, 2, 1, 96),
     (1, 13, 10, 1, 1, 2, 64), (1, 1, 257, 1, 1, 1, 64), (1, 16, 17, 1, 1, 1, 128), (1, 8, 8, 2, 4, 1, 112), (1, 6, 6, 2, 3, 2, 16),
+    # small maps in batches large enough for the dense mode
+    (37, 1, 1, 7, 9, 1, 64), (30, 2, 2, 4, 5, 4, 16), (60, 2, 4, 2, 3, 8, 16), (200, 1, 1, 3, 9, 1, 128), (23, 8, 1, 2, 4, 20, 48),
     (1, 16, 16, 1, 1, 1, 32), (1, 12, 11, 2, 3, 2, 64), (2, 16, 8, 2, 4, 1, 128), (1, 15, 9, 3, 5, 1, 64), (1, 1, 128, 1, 1, 2, 128),
     (1, 20, 13, 2, 3, 1, 128), (1, 8, 8, 3, 5, 2, 64), (1, 9, 9, 2, 2, 2, 16), (1, 11, 12, 2, 3, 1, 48), (1, 10, 7, 3, 4, 1, 112), (2, 8, 9, 2, 4, 1, 32), (1, 129, 1, 2, 2, 2, 64), (1, 1, 3, 16, 7, 1, 32), (2, 1, 2, 32, 5, 1, 16),
 ]
@@ -68,7 +70,7 @@ def test_bad_entries_and_empty_rows(dtype, rs):
     """Entries outside [0, R) contribute nothing and are flagged; a row with none left gives 0 and takes part
     in no gradient; a region that nothing routes to has gradients 0."""
     heads, n_win, topk, hd = 2, 3, 4, 64
-    q, k, v, idx, lam, dout = make(2, *rs, n_win, topk, heads, hd, dtype, 3)
+    q, k, v, idx, lam, dout = make(100 if rs == (1, 1) else 2, *rs, n_win, topk, heads, hd, dtype, 3)  # 100: the dense mode
     idx[idx == 5] = 4  # nothing routes to region 5
     idx[0, 2] = torch.tensor([-1, 9, 1 << 30, -(1 << 31)], dtype=torch.int32)
     idx[1, 7, 0], idx[1, 7, 3], idx[0, 0, 1] = -7, 9, 100
@@ -99,14 +101,14 @@ def test_bad_entries_and_empty_rows(dtype, rs):
 def test_not_finite_outside_the_routed_regions(dtype, rs):
     """NaN and infinities in a region that nobody routes to change nothing elsewhere."""
     heads, n_win, hd = 1, 3, 64
-    q, k, v, idx, lam, dout = make(1, *rs, n_win, 2, heads, hd, dtype, 4)
+    q, k, v, idx, lam, dout = make(200 if rs == (1, 1) else 1, *rs, n_win, 2, heads, hd, dtype, 4)  # 200: the dense mode
     idx[idx == 4] = 3
     want = ref.diff(q, k, v, idx, lam, heads, n_win, dout)
     tok = ref.region_tokens(q.shape[1], q.shape[2], n_win)
     for bad in (float("nan"), float("inf"), torch.finfo(dtype).min):
         k2, v2 = k.clone(), v.clone()
-        k2.view(-1, hd)[tok[4]] = bad
-        v2.view(-1, hd)[tok[4]] = bad
+        k2.view(len(q), -1, hd)[:, tok[4]] = bad
+        v2.view(len(q), -1, hd)[:, tok[4]] = bad
         out = bra.diff_attend(q, k2, v2, idx, lam, heads, n_win)
         ref.check(out, want["out"], want["out_tol"], f"{bad} out")
         for name, t in zip(("dq", "dk", "dv", "dlam"),
@@ -115,7 +117,7 @@ def test_not_finite_outside_the_routed_regions(dtype, rs):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("shape", [(1, 1, 1, 7, 5, 1, 64), (1, 4, 4, 3, 2, 1, 64), (1, 3, 4, 3, 7, 1, 32), (1, 9, 9, 2, 2, 1, 64), (1, 16, 15, 1, 1, 1, 128)],
+@pytest.mark.parametrize("shape", [(1, 1, 1, 7, 5, 1, 64), (37, 1, 1, 7, 5, 1, 64), (1, 4, 4, 3, 2, 1, 64), (1, 3, 4, 3, 7, 1, 32), (1, 9, 9, 2, 2, 1, 64), (1, 16, 15, 1, 1, 1, 128)],
                          ids=lambda s: "x".join(map(str, s)))
 def test_not_finite_scores_make_their_rows_nan(shape, dtype):
     """A NaN or infinite element of a query or a key: outputs and gradients are not finite exactly where the 64-bit
@@ -143,7 +145,7 @@ def test_not_finite_values_reach_their_own_queries(dtype):
     """One infinite value: the queries whose rows name its region get an infinity or NaN in that channel,
     all others and all other channels what they had."""
     for hr, wr, n_win, hd in ((1, 1, 7, 64), (2, 3, 3, 32), (4, 4, 3, 64), (9, 9, 2, 64)):
-        q, k, v, idx, lam, _ = make(2, hr, wr, n_win, 2, 1, hd, dtype, 40)
+        q, k, v, idx, lam, _ = make(40 if hr == 1 else 2, hr, wr, n_win, 2, 1, hd, dtype, 40)  # 40: the dense mode
         idx[1, 0] = 1  # one row that does not name region 0 and one that does
         idx[1, 1, 0] = 0
         before = bra.diff_attend(q, k, v, idx, lam, 1, n_win)
