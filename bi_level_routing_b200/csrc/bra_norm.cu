@@ -162,8 +162,8 @@ __device__ __forceinline__ float normalise(float (&z)[V * VPT], const NormArgs &
     return r;
 }
 
-// u becomes r (u - mean(u) - z^ mean(u z^)), the mean(u) term for LayerNorm only. Elements past the row
-// are 0 in z^ and u and are not stored, so what they become does not matter.
+// u becomes r (u - mean(u) - z^ mean(u z^)), the mean(u) term for LayerNorm only. Elements past the row are 0 in z^ and u on
+// the way in, not on the way out: the caller multiplies them by channel factors of 0 before it sums again.
 template <int TPR, int E>
 __device__ __forceinline__ void norm_back(float (&u)[E], const float (&z)[E], float r, const NormArgs &a, float *red, int &turn)
 {
@@ -180,7 +180,8 @@ __device__ __forceinline__ void norm_back(float (&u)[E], const float (&z)[E], fl
     for (int i = 0; i < E; i += 2) put(u + i, __ffma2_rn(pair(z + i), m1, __ffma2_rn(pair(u + i), rr, m0)));
 }
 
-// E values of a channel array at this thread's vectors; `def` where the array is absent or past the row.
+// E values of a channel array at this thread's vectors: `def` where the array is absent, 0 past the row (what is multiplied
+// by them must stay 0 there: the next sums run over it).
 template <int TPR, int V, int VPT>
 __device__ __forceinline__ void load_channels(float (&w)[V * VPT], const float *p, float def, int nvec, int lane)
 {
@@ -188,8 +189,9 @@ __device__ __forceinline__ void load_channels(float (&w)[V * VPT], const float *
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int j = 0; j < V / 4; ++j) {
-            float4 f = make_float4(def, def, def, def);
-            if (p && lane + i * TPR < nvec) f = __ldg(reinterpret_cast<const float4 *>(p) + (lane + i * TPR) * (V / 4) + j);
+            const bool in = lane + i * TPR < nvec;
+            float4 f = in ? make_float4(def, def, def, def) : make_float4(0.f, 0.f, 0.f, 0.f);
+            if (p && in) f = __ldg(reinterpret_cast<const float4 *>(p) + (lane + i * TPR) * (V / 4) + j);
             w[i * V + 4 * j] = f.x;
             w[i * V + 4 * j + 1] = f.y;
             w[i * V + 4 * j + 2] = f.z;

@@ -110,6 +110,15 @@ def near(got, want, size, steps, what):
     ref.check(got, want, torch.as_tensor(size, dtype=ref.F64).expand(want.shape) * steps * 2.0 ** -24, what)
 
 
+def close(got, want, what):
+    """The whole tensor: rounding the outputs moves each by at most half a step U of its value, so the difference's 2-norm is at most
+    U times the result's; the fp32 arithmetic before it (some hundred steps of 2^-24 at most, mostly not in one
+    direction) gets 2e-5 of it."""
+    u = torch.finfo(got.dtype).eps / 2
+    far = float((got.cpu().double() - want).norm()) / float(want.norm())
+    assert far <= u + 2e-5, f"{what}: {far:.2e} of the result's norm"
+
+
 def check_norms(a, alpha, eps, kind, with_ds=True):
     """Bounds. A mean of C values adds C roundings at most (trees add fewer), the mean of squares as many,
     so norm(h) is off by less than 2 C + 16 steps of its largest value + 1; s by that of |alpha x| + |gate p|.
@@ -137,9 +146,11 @@ def check_norms(a, alpha, eps, kind, with_ds=True):
     s_size = abs(alpha) * biggest(a["x"]) + top
     if s is not None:
         near(s, want["s"], s_size, steps, "s")
+        close(s, want["s"], "s")
     rs = max(spread(want["s"]), 1.0)
     if a["pre_weight"] is not None:
         near(y, want["y"], rs * 2 * s_size * biggest(a["pre_weight"]) + biggest(a["pre_bias"]), 2 * steps, "y")
+        close(y, want["y"], "y")
     dy = randn(a["x"].shape, 91, a["x"].dtype) if a["pre_weight"] is not None else None
     ds = randn(a["x"].shape, 92, a["x"].dtype) if with_ds or dy is None else None
     grads = bra.norm_residual_backward(a["x"], a["h"], dy, ds, *(a[m] for m in ("gate", "post_weight", "post_bias", "pre_weight", "pre_bias")),
@@ -160,6 +171,7 @@ def check_norms(a, alpha, eps, kind, with_ds=True):
             assert want.get(name) is None
             continue
         near(got, want[name], sizes[name], 4 * steps + (rows if name not in ("dx", "dh") else 0), name)
+        close(got, want[name], name)
 
 
 # C: one 16-byte vector, fewer threads than a warp, ragged vectors, one and several warps a row, the widest
