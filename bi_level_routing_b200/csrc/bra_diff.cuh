@@ -60,6 +60,9 @@ struct DiffArgs {
     FastDiv by_rs, by_wr, by_nwin, by_heads, by_tiles, by_R, by_topk;
 };
 
+// Warps of a CTA of 32 rows in the CUDA-core kernels of regions above 16 tokens.
+inline int diff_simt_warps(int topk, int rs) { return (long long)topk * rs <= 256 ? 4 : 8; }
+
 // Offset y W + x (in tokens, inside an image) of token `tok` of the region whose first token lies at
 // `base`.
 __device__ __forceinline__ int token_at(const DiffArgs &a, int base, int tok)

@@ -621,7 +621,7 @@ long long diff_backward_parts(const Geometry &g, DiffBackward kernels)
     else if (kernels == DiffBackward::kMma)
         per = g.rs <= 16 ? 1 : g.rs <= 32 ? 2 : 4LL * ((g.rs + 63) / 64);
     else
-        per = g.rs <= 16 ? 4 : 4LL * ((g.rs + 31) / 32);
+        per = g.rs <= 16 ? 4 : (long long)diff_simt_warps(g.topk, g.rs) * ((g.rs + 31) / 32);
     return (long long)g.B * g.R * per;
 }
 

@@ -52,7 +52,7 @@ __device__ __forceinline__ void lane_products(float (&acc)[RW][2], const float *
     float2 s[RW][2];
 #pragma unroll
     for (int i = 0; i < RW; ++i) s[i][0] = s[i][1] = make_float2(0.f, 0.f);
-#pragma unroll 1
+#pragma unroll (RW == 8 ? 1 : 2)
     for (int c = c0; c < c1; c += 4) {
         const float4 x = *reinterpret_cast<const float4 *>(t0 + c), y = *reinterpret_cast<const float4 *>(t1 + c);
 #pragma unroll
@@ -83,7 +83,7 @@ __device__ __forceinline__ void turn_products(float (&o)[RW][NC], const float *p
         float2 s[RW];
 #pragma unroll
         for (int i = 0; i < RW; ++i) s[i] = make_float2(0.f, 0.f);
-#pragma unroll 1
+#pragma unroll (RW == 8 ? 1 : 2)
         for (int j = 0; j < kTileRows; j += 4) {
             const float2 v0 = make_float2(tile[j * (hd + 4) + c], tile[(j + 1) * (hd + 4) + c]);
             const float2 v1 = make_float2(tile[(j + 2) * (hd + 4) + c], tile[(j + 3) * (hd + 4) + c]);
@@ -507,7 +507,10 @@ template <typename T, int NC> cudaError_t launch_nc(DiffArgs &a, bool backward, 
 {
     if (a.rs <= 4) return launch_one<T, 4, 1, NC>(a, backward, stream);
     if (a.rs <= 16) return launch_one<T, 4, 4, NC>(a, backward, stream);
-    return launch_one<T, 4, 8, NC>(a, backward, stream);
+    // CTAs of 32 rows: eight to a warp, whose reads feed the most FMAs, or, for many keys, twice the warps of four rows (3
+    // regions of 63 tokens, 48 channels: 47 and 53 us; one of 1024, 64 channels: 148 and 112 us)
+    if (diff_simt_warps(a.topk, a.rs) == 4) return launch_one<T, 4, 8, NC>(a, backward, stream);
+    return launch_one<T, 8, 4, NC>(a, backward, stream);
 }
 
 template <typename T> cudaError_t launch_t(DiffArgs &a, bool backward, cudaStream_t stream)
