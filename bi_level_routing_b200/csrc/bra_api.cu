@@ -724,11 +724,10 @@ static bra_status diff_attend_impl(const void *q, const void *k, const void *v, 
     a.lam = lambda;
     a.out = out;
     a.err = st->error_word;
-    const bool bf16 = dtype == BRA_BF16;
-    const cudaError_t e = bf16 && bra::diff_tile_supports(g)  ? bra::launch_diff_attend_tile(a, stream)
-                          : bf16 && bra::diff_umma_supports(g) ? bra::launch_diff_attend_umma(a, stream)
-                          : bf16 && bra::diff_mma_supports(g) ? bra::launch_diff_attend_mma(a, stream)
-                                                              : bra::launch_diff_simt(a, false, bf16, stream);
+    const cudaError_t e = dtype != BRA_BF16            ? bra::launch_diff_simt(a, false, stream)
+                          : bra::diff_tile_supports(g) ? bra::launch_diff_attend_tile(a, stream)
+                          : bra::diff_umma_supports(g) ? bra::launch_diff_attend_umma(a, stream)
+                                                       : bra::launch_diff_attend_mma(a, stream);
     return e == cudaSuccess ? BRA_OK : cuda_fail(e, "differential attention kernel");
 }
 
@@ -795,10 +794,9 @@ bra_status bra_diff_attend_backward(const void *q, const void *k, const void *v,
     if ((long long)g.N * topk > (1LL << 30)) return BRA_ERR_UNSUPPORTED;
     DeviceState *st = nullptr;
     if ((s = device_state(&st)) != BRA_OK) return s;
-    const bool bf16 = dtype == BRA_BF16;
-    const bra::DiffBackward kernels = bf16 && bra::diff_backward_umma_supports(g) ? bra::DiffBackward::kUmma
-                                      : bf16 && bra::diff_mma_supports(g)         ? bra::DiffBackward::kMma
-                                                                                  : bra::DiffBackward::kSimt;
+    const bra::DiffBackward kernels = dtype != BRA_BF16                     ? bra::DiffBackward::kSimt
+                                      : bra::diff_backward_umma_supports(g) ? bra::DiffBackward::kUmma
+                                                                            : bra::DiffBackward::kMma;
     bra::DiffArgs a = {};
     bra::diff_plan(a, g);
     const size_t stats = (size_t)B * heads * g.N * sizeof(float4);
@@ -829,7 +827,7 @@ bra_status bra_diff_attend_backward(const void *q, const void *k, const void *v,
     if (e == cudaSuccess)
         e = kernels == bra::DiffBackward::kUmma  ? bra::launch_diff_backward_umma(a, cs)
             : kernels == bra::DiffBackward::kMma ? bra::launch_diff_backward_mma(a, cs)
-                                                 : bra::launch_diff_simt(a, true, bf16, cs);
+                                                 : bra::launch_diff_simt(a, true, cs);
     const cudaError_t f = cudaFreeAsync(ws, cs);
     if (e != cudaSuccess) return cuda_fail(e, "differential backward kernels");
     if (f != cudaSuccess) return cuda_fail(f, "cudaFreeAsync(differential backward scratch)");

@@ -123,6 +123,28 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
 {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+__device__ __forceinline__ void cp_async8_or_zero(uint32_t dst, const void *src, bool real)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(real ? 8 : 0) : "memory");
+}
+// 16-byte chunk j of a row in shared memory: the head's two halves of d channels padded with zeros to DK each (q, k), or its hd
+// channels run on, zeros after them (v, dout). src: the head's first channel of the token. Halves that are not whole
+// 16-byte chunks (d a multiple of 4) are copied in pieces of 8 bytes.
+template <int DK>
+__device__ __forceinline__ void copy_split(uint32_t row, const __nv_bfloat16 *src, int j, int d, bool real)
+{
+    const int m = j / (DK / 8), x = 8 * (j % (DK / 8));
+    if (d % 8 == 0) {
+        cp_async16_or_zero(row + 16 * j, src + (x < d ? m * d + x : 0), real && x < d);
+    } else {
+        cp_async8_or_zero(row + 16 * j, src + (x < d ? m * d + x : 0), real && x < d);
+        cp_async8_or_zero(row + 16 * j + 8, src + (x + 4 < d ? m * d + x + 4 : 0), real && x + 4 < d);
+    }
+}
+__device__ __forceinline__ void copy_run(uint32_t row, const __nv_bfloat16 *src, int j, int hd, bool real)
+{
+    cp_async16_or_zero(row + 16 * j, src + (8 * j < hd ? 8 * j : 0), real && 8 * j < hd);
+}
 template <int N> __device__ __forceinline__ void cp_async_wait_but()
 {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");

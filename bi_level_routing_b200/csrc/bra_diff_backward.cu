@@ -1,5 +1,5 @@
 // bra_diff_backward.cu -- gradients of differential attention for bf16 maps on mma.sync (formula in
-// bra_diff.cuh), heads of 16 to 128 channels in multiples of 16, regions of any size.
+// bra_diff.cuh), heads of 8 to 128 channels in multiples of 8, regions of any size.
 //
 // Nothing is added in memory, so the gradients are the same bits on every run:
 //  invert   lists for each region s the regions that route to it, in the order (region, slot);
@@ -14,7 +14,8 @@
 //           the launch's first `heads` CTAs also add up dlam from the partial sums.
 //
 // Precision: S and dP are exact products of bf16 in fp32 sums, statistics and accumulators are
-// fp32; P and dS enter the last products as bf16; each gradient is rounded to bf16 once.
+// fp32. P and, for dk, dS enter the last products as bf16. A row's dS sum to 0, so its roundings meet all of k, of which dq keeps
+// only what differs between keys: for dq, dS is two bf16 terms. Each gradient is rounded to bf16 once.
 #include "bra_diff.cuh"
 
 namespace bra {
@@ -36,19 +37,6 @@ template <int DK> struct BackTile {
     static constexpr int kLanes = pow2_at_least(kHp / 8);
     static constexpr int kNk = DK / 16;
 };
-
-// 16-byte chunk j (of the hd / 8 real ones) of a row whose two halves are padded to DK channels each.
-template <int DK> __device__ __forceinline__ int padded_chunk(int j, int dc) { return j < dc ? j : DK / 8 + j - dc; }
-
-// Clears the channels between d and DK of `rows` rows.
-template <int DK> __device__ __forceinline__ void clear_padding(__nv_bfloat16 *tile, int rows, int dc, int tid, int threads)
-{
-    constexpr int ROW = BackTile<DK>::kRow;
-    for (int e = tid; e < rows * (2 * DK / 8); e += threads) {
-        const int c = e % (2 * DK / 8);
-        if (c % (DK / 8) >= dc) *reinterpret_cast<uint4 *>(tile + (e / (2 * DK / 8)) * ROW + 8 * c) = make_uint4(0, 0, 0, 0);
-    }
-}
 
 // The A fragments of rows g and g + 8 (in-region tokens tok0 + ...) of a [.., C] array: NF steps of 16
 // channels. split: the two halves of d channels are padded to NF / 2 steps each; else hd channels run on.
@@ -111,6 +99,18 @@ __device__ __forceinline__ void pack_step(uint32_t (&p)[4], const float (&lo)[4]
     p[3] = pack_bf16x2(hi[2], hi[3]);
 }
 
+// The same in two bf16 terms: the values with their low 16 bits cleared, and the rest rounded (16 significant bits in all).
+__device__ __forceinline__ void split_step(uint32_t (&hi)[4], uint32_t (&lo)[4], const float (&x)[4], const float (&y)[4])
+{
+    const float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = bf16_trunc(v[2 * i]), b = bf16_trunc(v[2 * i + 1]);
+        hi[i] = pack_bf16x2_trunc(a, b);
+        lo[i] = pack_bf16x2(v[2 * i] - a, v[2 * i + 1] - b);
+    }
+}
+
 // A warp's 16 accumulator rows, scaled and rounded, through its own shared-memory rows to
 // whole-row stores. Column tiles [0, DK / 8) are the first half's channels, the others the second's
 // (split) or the channels run on.
@@ -119,7 +119,7 @@ __device__ __forceinline__ void store_rows(const DiffArgs &a, __nv_bfloat16 *bas
                                            __nv_bfloat16 *rows, const float (&acc)[DK / 4][4], bool split, float s0, float s1)
 {
     constexpr int ROW = BackTile<DK>::kRow;
-    const int g = lane >> 2, t = lane & 3, dc = a.d / 8;
+    const int g = lane >> 2, t = lane & 3;
     __syncwarp();
 #pragma unroll
     for (int nt = 0; nt < DK / 4; ++nt) {
@@ -130,13 +130,17 @@ __device__ __forceinline__ void store_rows(const DiffArgs &a, __nv_bfloat16 *bas
     __syncwarp();
     constexpr int lanes = BackTile<DK>::kLanes;
     const int j = lane % lanes;
-    if (j < 2 * dc) {
-        const int c = split ? padded_chunk<DK>(j, dc) : j;
+    if (8 * j < a.hd) {
+        // where the chunk's two groups of four channels stand in the row
+        const int c0 = split && 8 * j >= a.d ? DK + 8 * j - a.d : 8 * j;
+        const int c1 = split && 8 * j + 4 >= a.d ? DK + 8 * j + 4 - a.d : 8 * j + 4;
         for (int row = lane / lanes; row < 16; row += 32 / lanes) {
             const int tok = tok0 + row;
-            if (tok < a.rs)
-                *reinterpret_cast<uint4 *>(base + (int64_t)token_at(a, region, tok) * a.C + 8 * j) =
-                    *reinterpret_cast<const uint4 *>(rows + row * ROW + 8 * c);
+            if (tok < a.rs) {
+                const uint2 lo = *reinterpret_cast<const uint2 *>(rows + row * ROW + c0);
+                const uint2 hi = *reinterpret_cast<const uint2 *>(rows + row * ROW + c1);
+                *reinterpret_cast<uint4 *>(base + (int64_t)token_at(a, region, tok) * a.C + 8 * j) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            }
         }
     }
 }
@@ -238,8 +242,6 @@ __global__ void __launch_bounds__(32 * kWarps, SINGLE && DK <= 32 ? 3 : 1) diff_
         const int n = gather_bases(a, a.idx + ((int64_t)it.b * a.R + it.r) * a.topk, bases, lane);
         if (lane == 0) *count = n;
     }
-    const int dc = a.d / 8;
-    if (a.d < DK) clear_padding<DK>(tiles, 2 * kStages * KT, dc, gtid, 32 * WPI);
     group_barrier<WPI>(group);
     const int nkeys = *count * a.rs;
     const int ntiles = (nkeys + KT - 1) / KT;
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(32 * kWarps, SINGLE && DK <= 32 ? 3 : 1) diff_
     const __nv_bfloat16 *gk = static_cast<const __nv_bfloat16 *>(a.k) + image;
     const __nv_bfloat16 *gv = static_cast<const __nv_bfloat16 *>(a.v) + image;
     auto fetch = [&](int tile, int stage) {
-        const int j = lane % L::kLanes, jk = padded_chunk<DK>(j, dc), r0 = tile * KT + wg * (KT / WPI);
+        const int j = lane % L::kLanes, r0 = tile * KT + wg * (KT / WPI);
         __nv_bfloat16 *sk = tiles + (size_t)stage * 2 * KT * ROW + wg * (KT / WPI) * ROW, *sv = sk + KT * ROW;
         warp_rows<KT / WPI, L::kLanes>(
             lane,
@@ -258,10 +260,10 @@ __global__ void __launch_bounds__(32 * kWarps, SINGLE && DK <= 32 ? 3 : 1) diff_
                 return token_at(a, bases[slot], tok);
             },
             [&](int row, int at) {
-                if (j >= 2 * dc) return;
-                const int64_t off = (int64_t)max(at, 0) * a.C + 8 * j;
-                cp_async16_or_zero(smem_u32(sk + row * ROW + 8 * jk), gk + off, at >= 0);
-                cp_async16_or_zero(smem_u32(sv + row * ROW + 8 * j), gv + off, at >= 0);
+                if (j >= HP / 8) return;
+                const int64_t off = (int64_t)max(at, 0) * a.C;
+                copy_split<DK>(smem_u32(sk + row * ROW), gk + off, j, a.d, at >= 0);
+                copy_run(smem_u32(sv + row * ROW), gv + off, j, a.hd, at >= 0);
             });
         cp_async_commit();
     };
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(32 * kWarps, SINGLE && DK <= 32 ? 3 : 1) diff_
     uint32_t qf[2 * NK][4], df[2 * NK][4];
     load_rows<2 * NK>(a, static_cast<const __nv_bfloat16 *>(a.q) + image, region, tok0, lane, true, qf);
     load_rows<2 * NK>(a, static_cast<const __nv_bfloat16 *>(a.dout) + image, region, tok0, lane, false, df);
-    const int vsteps = a.hd / 16;
+    const int vsteps = (a.hd + 15) / 16;
 
     float s[2][NT][4], dp[NT][4];
     // S1, S2 and dP of the warp's rows against the tile in `stage`
@@ -387,19 +389,21 @@ __global__ void __launch_bounds__(32 * kWarps, SINGLE && DK <= 32 ? 3 : 1) diff_
                     const float p = SINGLE ? s[m][nt][i] * l[m][i >> 1] : fast_exp2(fmaf(s[m][nt][i], a.scale_log2, -Ls[m][i >> 1]));
                     s[m][nt][i] = p * (dp[nt][i] - D[m][i >> 1]);
                 }
-            uint32_t pf[KT / 16][4];
 #pragma unroll
-            for (int ks = 0; ks < KT / 16; ++ks) pack_step(pf[ks], s[m][2 * ks], s[m][2 * ks + 1]);
+            for (int ks = 0; ks < KT / 16; ++ks) {
+                uint32_t hi[4], lo[4];
+                split_step(hi, lo, s[m][2 * ks], s[m][2 * ks + 1]);
 #pragma unroll
-            for (int np = 0; np < DK / 16; ++np)
-#pragma unroll
-                for (int ks = 0; ks < KT / 16; ++ks) {
+                for (int np = 0; np < DK / 16; ++np) {
                     uint32_t b[4];
                     ldmatrix_x4_trans(k0 + ((16 * ks + (lane & 15)) * ROW + m * DK + 16 * np + 8 * (lane >> 4)) * 2, b[0],
                                       b[1], b[2], b[3]);
-                    mma_bf16_16816(acc[m * (DK / 8) + 2 * np], pf[ks], b[0], b[1]);
-                    mma_bf16_16816(acc[m * (DK / 8) + 2 * np + 1], pf[ks], b[2], b[3]);
+                    mma_bf16_16816(acc[m * (DK / 8) + 2 * np], hi, b[0], b[1]);
+                    mma_bf16_16816(acc[m * (DK / 8) + 2 * np + 1], hi, b[2], b[3]);
+                    mma_bf16_16816(acc[m * (DK / 8) + 2 * np], lo, b[0], b[1]);
+                    mma_bf16_16816(acc[m * (DK / 8) + 2 * np + 1], lo, b[2], b[3]);
                 }
+            }
         }
     }
     group_barrier<WPI>(group);  // every warp has left the tiles: the rows go through them
@@ -442,8 +446,6 @@ __global__ void __launch_bounds__(32 * kWarps, DK <= 32 ? 3 : 1) diff_backward_k
     }
     if (item >= a.nitems) return;  // the whole group
     const DiffItem it = diff_item(a, item);
-    const int dc = a.d / 8;
-    if (a.d < DK) clear_padding<DK>(tiles, 4 * QT, dc, gtid, 32 * WPI);
     const int32_t *start = a.start + (int64_t)it.b * (a.R + 1) + it.r;
     const int first = __ldg(start);
     // the gathered queries: their count passes 31 bits only where a region is named more than
@@ -455,9 +457,8 @@ __global__ void __launch_bounds__(32 * kWarps, DK <= 32 ? 3 : 1) diff_backward_k
     const __nv_bfloat16 *gq = static_cast<const __nv_bfloat16 *>(a.q) + image;
     const __nv_bfloat16 *gd = static_cast<const __nv_bfloat16 *>(a.dout) + image;
     const float4 *stats = a.stats + ((int64_t)it.b * a.heads + it.h) * a.N;
-    if (a.d < DK) group_barrier<WPI>(group);
     auto fetch = [&](int tile, int stage) {
-        const int j = lane % L::kLanes, jq = padded_chunk<DK>(j, dc), own = wg * (QT / WPI), r0 = tile * QT + own;
+        const int j = lane % L::kLanes, own = wg * (QT / WPI), r0 = tile * QT + own;
         __nv_bfloat16 *sq = tiles + (size_t)stage * 2 * QT * ROW + own * ROW, *sd = sq + QT * ROW;
         warp_rows<QT / WPI, L::kLanes>(
             lane,
@@ -469,10 +470,10 @@ __global__ void __launch_bounds__(32 * kWarps, DK <= 32 ? 3 : 1) diff_backward_k
             },
             [&](int row, int at) {
                 if (j == 0) cp_async16_or_zero(smem_u32(sstat + stage * QT + own + row), stats + max(at, 0), at >= 0);
-                if (j >= 2 * dc) return;
-                const int64_t off = (int64_t)max(at, 0) * a.C + 8 * j;
-                cp_async16_or_zero(smem_u32(sq + row * ROW + 8 * jq), gq + off, at >= 0);
-                cp_async16_or_zero(smem_u32(sd + row * ROW + 8 * j), gd + off, at >= 0);
+                if (j >= HP / 8) return;
+                const int64_t off = (int64_t)max(at, 0) * a.C;
+                copy_split<DK>(smem_u32(sq + row * ROW), gq + off, j, a.d, at >= 0);
+                copy_run(smem_u32(sd + row * ROW), gd + off, j, a.hd, at >= 0);
             });
         cp_async_commit();
     };
@@ -484,7 +485,7 @@ __global__ void __launch_bounds__(32 * kWarps, DK <= 32 ? 3 : 1) diff_backward_k
     uint32_t kf[2 * NK][4], vf[2 * NK][4];
     load_rows<2 * NK>(a, static_cast<const __nv_bfloat16 *>(a.k) + image, region, tok0, lane, true, kf);
     load_rows<2 * NK>(a, static_cast<const __nv_bfloat16 *>(a.v) + image, region, tok0, lane, false, vf);
-    const int vsteps = a.hd / 16;
+    const int vsteps = (a.hd + 15) / 16;
     const float lam = __ldg(a.lam + it.h);
 
     float dk[HP / 8][4], dv[HP / 8][4];

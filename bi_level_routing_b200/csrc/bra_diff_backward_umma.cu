@@ -7,7 +7,7 @@
 //
 // queries: a CTA owns 128 queries. S1, S2 and dP = dout V^T of every key tile are formed twice: first for both
 //   softmaxes' maximum and sum and D_i = rowsum(P_i dP), which the warpgroups take over their own tiles and merge, then
-//   for dS_i, written as bf16 over S_i in TMEM and multiplied from there: dq_i += dS_i K_i.
+//   for dS_i, written as two bf16 terms over S_i and dP in TMEM and multiplied from there: dq_i += dS_i K_i.
 // keys: a CTA owns 128 keys and meets the queries that route to them. S_i and dP are formed transposed (keys as
 //   rows), so that P1 - lam P2 and dS_i again multiply from where they were scored: dv += (P1 - lam P2)^T dout,
 //   dk_i += dS_i^T q_i.
@@ -260,8 +260,11 @@ template <int NB> __global__ void __launch_bounds__(kThreads, 1) diff_backward_q
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int ks = 0; ks < T / 16; ++ks)
-                        umma_ts(tm + 384 + 32 * NB * m, tm + 192 * buf + 64 * m + 8 * ks,
-                                rk + (NB == 1 ? 4 * m : m * (kBlock >> 4)) + 128 * ks, kIdescQ, i > n || ks > 0);
+#pragma unroll
+                        for (int term = 0; term < 2; ++term)  // dS's high terms over S_m, its low ones over dP
+                            umma_ts(tm + 384 + 32 * NB * m,
+                                    tm + 192 * buf + (term ? 128 + 32 * (ks / 2) + 16 * m + 8 * (ks % 2) : 64 * m + 8 * ks),
+                                    rk + (NB == 1 ? 4 * m : m * (kBlock >> 4)) + 128 * ks, kIdescQ, i > n || ks > 0 || term > 0);
             }
             if (i + 2 < all) scores(buf);
             if (leader) {
@@ -369,7 +372,7 @@ template <int NB> __global__ void __launch_bounds__(kThreads, 1) diff_backward_q
                     tmem_ld_32x32(t_s + 64 + c, s2);
                     tmem_ld_32x32(t_s + 128 + c, dp);
                     tmem_wait_ld();
-                    uint32_t w1[16], w2[16];
+                    uint32_t w1[16], w2[16], low[32];  // dS1, dS2: high terms; low terms of 1, then of 2
 #pragma unroll
                     for (int x = 0; x < 32; x += 2) {
                         float2 ds[2];
@@ -379,22 +382,29 @@ template <int NB> __global__ void __launch_bounds__(kThreads, 1) diff_backward_q
                             const float2 z = __ffma2_rn(make_float2(__uint_as_float(s1[x + y]), __uint_as_float(s2[x + y])), sc, nl);
                             ds[y] = __fmul2_rn(make_float2(fast_exp2(z.x), fast_exp2(z.y)), __fadd2_rn(make_float2(dpx, dpx), nd));
                         }
-                        w1[x / 2] = pack_bf16x2(ds[0].x, ds[1].x);
-                        w2[x / 2] = pack_bf16x2(ds[0].y, ds[1].y);
+                        const float h0 = bf16_trunc(ds[0].x), h1 = bf16_trunc(ds[1].x);
+                        const float g0 = bf16_trunc(ds[0].y), g1 = bf16_trunc(ds[1].y);
+                        w1[x / 2] = pack_bf16x2_trunc(h0, h1);
+                        w2[x / 2] = pack_bf16x2_trunc(g0, g1);
+                        low[x / 2] = pack_bf16x2(ds[0].x - h0, ds[1].x - h1);
+                        low[16 + x / 2] = pack_bf16x2(ds[0].y - g0, ds[1].y - g1);
                     }
                     if ((i - ntiles + 1) * T > nkeys) {  // keys past the last one: their rows of k are zeros, their dS must be finite
 #pragma unroll
                         for (int x = 0; x < 16; ++x) {
                             const int key = (i - ntiles) * T + c + 2 * x;
-                            if (key >= nkeys) w1[x] = w2[x] = 0u;
+                            if (key >= nkeys) w1[x] = w2[x] = low[x] = low[16 + x] = 0u;
                             if (key + 1 == nkeys) {
                                 w1[x] &= 0xffffu;
                                 w2[x] &= 0xffffu;
+                                low[x] &= 0xffffu;
+                                low[16 + x] &= 0xffffu;
                             }
                         }
                     }
                     tmem_st_32x16(t_s + c / 2, w1);
                     tmem_st_32x16(t_s + 64 + c / 2, w2);
+                    tmem_st_32x32(t_s + 128 + c, low);
                 }
                 tmem_wait_st();
             }
@@ -650,7 +660,7 @@ template <int NB> __global__ void __launch_bounds__(kThreads, 1) diff_backward_k
     if (warp == 8) tmem_dealloc(tmem, kCols);
 }
 
-bool diff_backward_umma_supports(const Geometry &g) { return diff_mma_supports(g) && g.rs > 64; }
+bool diff_backward_umma_supports(const Geometry &g) { return g.hd % 16 == 0 && g.rs > 64; }
 
 namespace {
 

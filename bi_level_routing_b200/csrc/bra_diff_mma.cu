@@ -1,5 +1,5 @@
 // bra_diff_mma.cu -- forward differential attention of bf16 maps on mma.sync (see bra_diff.cuh for
-// the formula), heads of 16 to 128 channels in multiples of 16, regions of any size.
+// the formula), heads of 8 to 128 channels in multiples of 8, regions of any size.
 //
 // One pass over the routed keys with the running maximum and sum of both softmaxes. A group of WPI
 // warps owns 16 WPI query tokens of one (image, region, head); each warp keeps 16 query rows, its
@@ -57,14 +57,6 @@ __global__ void __launch_bounds__(32 * kWarps) diff_attend_mma_kernel(const Diff
         const int n = gather_bases(a, a.idx + ((int64_t)it.b * a.R + it.r) * a.topk, bases, lane);
         if (lane == 0) *count = n;
     }
-    const int dc = a.d / 8;  // 16-byte chunks of a half head
-    if (a.d < DK) {          // channels between d and DK multiply zeros: cleared once, no copy lands there
-        for (int e = gtid; e < 4 * KT * (HP / 8); e += 32 * WPI) {
-            const int c = e % (HP / 8);
-            if (c % (DK / 8) >= dc)
-                *reinterpret_cast<uint4 *>(tiles + (e / (HP / 8)) * ROW + 8 * c) = make_uint4(0, 0, 0, 0);
-        }
-    }
     group_barrier<WPI>(group);
     const int nkeys = *count * a.rs;
     const int ntiles = (nkeys + KT - 1) / KT;
@@ -73,7 +65,7 @@ __global__ void __launch_bounds__(32 * kWarps) diff_attend_mma_kernel(const Diff
     const __nv_bfloat16 *gk = static_cast<const __nv_bfloat16 *>(a.k) + image;
     const __nv_bfloat16 *gv = static_cast<const __nv_bfloat16 *>(a.v) + image;
     auto fetch = [&](int tile, int stage) {
-        const int j = lane % L::kLanes, jk = j < dc ? j : DK / 8 + j - dc, r0 = tile * KT + wg * (KT / WPI);
+        const int j = lane % L::kLanes, r0 = tile * KT + wg * (KT / WPI);
         __nv_bfloat16 *sk = tiles + (size_t)stage * 2 * KT * ROW + wg * (KT / WPI) * ROW, *sv = sk + KT * ROW;
         warp_rows<KT / WPI, L::kLanes>(
             lane,
@@ -84,10 +76,10 @@ __global__ void __launch_bounds__(32 * kWarps) diff_attend_mma_kernel(const Diff
                 return token_at(a, bases[slot], tok);
             },
             [&](int row, int at) {
-                if (j >= 2 * dc) return;
-                const int64_t off = (int64_t)max(at, 0) * a.C + 8 * j;
-                cp_async16_or_zero(smem_u32(sk + row * ROW + 8 * jk), gk + off, at >= 0);
-                cp_async16_or_zero(smem_u32(sv + row * ROW + 8 * j), gv + off, at >= 0);
+                if (j >= HP / 8) return;
+                const int64_t off = (int64_t)max(at, 0) * a.C;
+                copy_split<DK>(smem_u32(sk + row * ROW), gk + off, j, a.d, at >= 0);
+                copy_run(smem_u32(sv + row * ROW), gv + off, j, a.hd, at >= 0);
             });
         cp_async_commit();
     };
@@ -231,7 +223,7 @@ __global__ void __launch_bounds__(32 * kWarps) diff_attend_mma_kernel(const Diff
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + image;
     constexpr int lanes = L::kLanes < 32 ? L::kLanes : 32;
     const int j = lane % lanes;
-    if (j < 2 * dc)
+    if (8 * j < a.hd)
         for (int row = lane / lanes; row < 16; row += 32 / lanes) {
             const int tok = tok0 + row;
             if (tok < a.rs)
@@ -239,8 +231,6 @@ __global__ void __launch_bounds__(32 * kWarps) diff_attend_mma_kernel(const Diff
                     *reinterpret_cast<const uint4 *>(rows + row * ROW + 8 * j);
         }
 }
-
-bool diff_mma_supports(const Geometry &g) { return g.hd % 16 == 0 && g.hd <= 128; }
 
 namespace {
 

@@ -1,6 +1,6 @@
-// bra_diff_simt.cu -- differential attention and its gradients on CUDA cores (formula in
-// bra_diff.cuh): fp32 maps, and bf16 heads whose halves are not whole 16-byte chunks. fp32
-// throughout, hd a multiple of 8 up to 128, regions of any size.
+// bra_diff_simt.cu -- differential attention and its gradients of fp32 maps on CUDA cores (formula in bra_diff.cuh), hd a
+// multiple of 8 up to 128, regions of any size. The FMA pipe bounds it: 6 hd operations a query-key pair forward, 18 hd
+// backward (both passes score again).
 //
 // A CTA owns WARPS x RW token rows of one (image, region, head), RW of them a warp's; the tokens they
 // meet (keys for the forward pass and dq, queries for dk and dv) come through shared memory in tiles of
@@ -26,21 +26,11 @@ template <int WARPS, int RW> struct SimtTile {
     }
 };
 
-// Row `row` of a [rows][hd + 4] fp32 tile from the hd channels at src (16-byte vectors), or zeros.
-template <typename T>
-__device__ __forceinline__ void stage_vector(float *tile, int hd, int row, int u, const T *src, bool real)
+// Channels 4 u .. of row `row` of a [rows][hd + 4] tile, or zeros.
+__device__ __forceinline__ void stage_vector(float *tile, int hd, int row, int u, const float *src, bool real)
 {
-    constexpr int V = Vec16<T>::N;
-    float f[V];
-    if (real) {
-        Vec16<T>::load(src + u * V, f);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = 0.f;
-    }
-    float4 *dst = reinterpret_cast<float4 *>(tile + row * (hd + 4) + u * V);
-#pragma unroll
-    for (int i = 0; i < V / 4; ++i) dst[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+    *reinterpret_cast<float4 *>(tile + row * (hd + 4) + 4 * u) =
+        real ? __ldg(reinterpret_cast<const float4 *>(src) + u) : make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
 // acc[i][0..1] += rows[i] . tile[lane], tile[lane + 32] over channels [c0, c1); packed over pairs of channels
@@ -108,12 +98,12 @@ template <int RW, int M> __device__ __forceinline__ void clear(float (&x)[RW][M]
 
 }  // namespace
 
-template <typename T, int WARPS, int RW, int NC>
+template <int WARPS, int RW, int NC>
 __global__ void __launch_bounds__(32 * WARPS) diff_attend_simt_kernel(const DiffArgs a)
 {
     constexpr int ROWS = WARPS * RW, THREADS = 32 * WARPS;
     extern __shared__ float4 smem4[];
-    const int hd = a.hd, stride = hd + 4, nvec = hd / Vec16<T>::N;
+    const int hd = a.hd, stride = hd + 4, nvec = hd / 4;
     float *sk = reinterpret_cast<float *>(smem4), *sv = sk + kTileRows * stride, *sq = sv + kTileRows * stride;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float *sp = sq + ROWS * stride + warp * 2 * RW * kTileRows;  // [map][RW][64]
@@ -121,8 +111,8 @@ __global__ void __launch_bounds__(32 * WARPS) diff_attend_simt_kernel(const Diff
     int *bases = count + 4;
     const DiffItem it = diff_item(a, blockIdx.x);
     const int64_t image = (int64_t)it.b * a.N * a.C + it.h * hd;
-    const T *gq = static_cast<const T *>(a.q) + image, *gk = static_cast<const T *>(a.k) + image;
-    const T *gv = static_cast<const T *>(a.v) + image;
+    const float *gq = static_cast<const float *>(a.q) + image, *gk = static_cast<const float *>(a.k) + image;
+    const float *gv = static_cast<const float *>(a.v) + image;
     const int region = region_at(a, it.r);
     grid_dependency_wait();
     if (warp == 0) {
@@ -132,7 +122,7 @@ __global__ void __launch_bounds__(32 * WARPS) diff_attend_simt_kernel(const Diff
     for (int e = threadIdx.x; e < ROWS * nvec; e += THREADS) {
         const int row = e / nvec, tok = it.t * ROWS + row;
         const bool in = tok < a.rs;
-        stage_vector<T>(sq, hd, row, e % nvec, gq + (int64_t)(in ? token_at(a, region, tok) : 0) * a.C, in);
+        stage_vector(sq, hd, row, e % nvec, gq + (int64_t)(in ? token_at(a, region, tok) : 0) * a.C, in);
     }
     __syncthreads();
     const int nkeys = *count * a.rs;
@@ -160,8 +150,8 @@ __global__ void __launch_bounds__(32 * WARPS) diff_attend_simt_kernel(const Diff
                 a.by_rs.divmod(key, slot, tok);
                 off = (int64_t)token_at(a, bases[slot], tok) * a.C;
             }
-            stage_vector<T>(sk, hd, row, e % nvec, gk + off, real);
-            stage_vector<T>(sv, hd, row, e % nvec, gv + off, real);
+            stage_vector(sk, hd, row, e % nvec, gk + off, real);
+            stage_vector(sv, hd, row, e % nvec, gv + off, real);
         }
         __syncthreads();
         if (!busy) continue;
@@ -194,28 +184,28 @@ __global__ void __launch_bounds__(32 * WARPS) diff_attend_simt_kernel(const Diff
     }
     if (!busy) return;
     const float lam = __ldg(a.lam + it.h);
-    T *out = static_cast<T *>(a.out) + image;
+    float *out = static_cast<float *>(a.out) + image;
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
         const int tok = it.t * ROWS + warp * RW + i;
         if (tok >= a.rs) break;
         const float w1 = over_sum(1.f, warp_sum(l[0][i]), nkeys > 0), w2 = over_sum(-lam, warp_sum(l[1][i]), nkeys > 0);
-        T *dst = out + (int64_t)token_at(a, region, tok) * a.C;
+        float *dst = out + (int64_t)token_at(a, region, tok) * a.C;
 #pragma unroll
         for (int cc = 0; cc < NC; ++cc) {
             const int c = lane + 32 * cc;
-            if (c < hd) dst[c] = from_float<T>(fmaf(o[0][i][cc], w1, o[1][i][cc] * w2));
+            if (c < hd) dst[c] = (fmaf(o[0][i][cc], w1, o[1][i][cc] * w2));
         }
     }
 }
 
 // dq and the statistics (see bra_diff_backward.cu)
-template <typename T, int WARPS, int RW, int NC>
+template <int WARPS, int RW, int NC>
 __global__ void __launch_bounds__(32 * WARPS) diff_backward_queries_simt_kernel(const DiffArgs a)
 {
     constexpr int ROWS = WARPS * RW, THREADS = 32 * WARPS;
     extern __shared__ float4 smem4[];
-    const int hd = a.hd, stride = hd + 4, nvec = hd / Vec16<T>::N;
+    const int hd = a.hd, stride = hd + 4, nvec = hd / 4;
     float *sk = reinterpret_cast<float *>(smem4), *sv = sk + kTileRows * stride, *sq = sv + kTileRows * stride;
     float *sd = sq + ROWS * stride;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -224,8 +214,8 @@ __global__ void __launch_bounds__(32 * WARPS) diff_backward_queries_simt_kernel(
     int *bases = count + 4;
     const DiffItem it = diff_item(a, blockIdx.x);
     const int64_t image = (int64_t)it.b * a.N * a.C + it.h * hd;
-    const T *gq = static_cast<const T *>(a.q) + image, *gk = static_cast<const T *>(a.k) + image;
-    const T *gv = static_cast<const T *>(a.v) + image, *gd = static_cast<const T *>(a.dout) + image;
+    const float *gq = static_cast<const float *>(a.q) + image, *gk = static_cast<const float *>(a.k) + image;
+    const float *gv = static_cast<const float *>(a.v) + image, *gd = static_cast<const float *>(a.dout) + image;
     const int region = region_at(a, it.r);
     grid_dependency_wait();
     if (warp == 0) {
@@ -236,8 +226,8 @@ __global__ void __launch_bounds__(32 * WARPS) diff_backward_queries_simt_kernel(
         const int row = e / nvec, tok = it.t * ROWS + row;
         const bool in = tok < a.rs;
         const int64_t off = (int64_t)(in ? token_at(a, region, tok) : 0) * a.C;
-        stage_vector<T>(sq, hd, row, e % nvec, gq + off, in);
-        stage_vector<T>(sd, hd, row, e % nvec, gd + off, in);
+        stage_vector(sq, hd, row, e % nvec, gq + off, in);
+        stage_vector(sd, hd, row, e % nvec, gd + off, in);
     }
     __syncthreads();
     const int nkeys = *count * a.rs;
@@ -254,8 +244,8 @@ __global__ void __launch_bounds__(32 * WARPS) diff_backward_queries_simt_kernel(
                 a.by_rs.divmod(key, slot, tok);
                 off = (int64_t)token_at(a, bases[slot], tok) * a.C;
             }
-            stage_vector<T>(sk, hd, row, e % nvec, gk + off, real);
-            stage_vector<T>(sv, hd, row, e % nvec, gv + off, real);
+            stage_vector(sk, hd, row, e % nvec, gk + off, real);
+            stage_vector(sv, hd, row, e % nvec, gv + off, real);
         }
     };
     float mx[2][RW], l[2][RW], ed[2][RW];
@@ -344,27 +334,27 @@ __global__ void __launch_bounds__(32 * WARPS) diff_backward_queries_simt_kernel(
     }
     if (!busy) return;
     const float s1 = a.scale, s2 = -__ldg(a.lam + it.h) * a.scale;
-    T *out = static_cast<T *>(a.dq) + image;
+    float *out = static_cast<float *>(a.dq) + image;
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
         const int tok = it.t * ROWS + warp * RW + i;
         if (tok >= a.rs) break;
-        T *dst = out + (int64_t)token_at(a, region, tok) * a.C;
+        float *dst = out + (int64_t)token_at(a, region, tok) * a.C;
 #pragma unroll
         for (int cc = 0; cc < NC; ++cc) {
             const int c = lane + 32 * cc;
-            if (c < hd) dst[c] = from_float<T>(dq[i][cc] * (c < a.d ? s1 : s2));
+            if (c < hd) dst[c] = (dq[i][cc] * (c < a.d ? s1 : s2));
         }
     }
 }
 
 // dk, dv and dlam (see bra_diff_backward.cu)
-template <typename T, int WARPS, int RW, int NC>
+template <int WARPS, int RW, int NC>
 __global__ void __launch_bounds__(32 * WARPS) diff_backward_keys_simt_kernel(const DiffArgs a)
 {
     constexpr int ROWS = WARPS * RW, THREADS = 32 * WARPS;
     extern __shared__ float4 smem4[];
-    const int hd = a.hd, stride = hd + 4, nvec = hd / Vec16<T>::N;
+    const int hd = a.hd, stride = hd + 4, nvec = hd / 4;
     float *sq = reinterpret_cast<float *>(smem4), *sd = sq + kTileRows * stride, *sk = sd + kTileRows * stride;
     float *sv = sk + ROWS * stride;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -387,8 +377,8 @@ __global__ void __launch_bounds__(32 * WARPS) diff_backward_keys_simt_kernel(con
     if (blockIdx.x >= a.nitems) return;
     const DiffItem it = diff_item(a, blockIdx.x);
     const int64_t image = (int64_t)it.b * a.N * a.C + it.h * hd;
-    const T *gq = static_cast<const T *>(a.q) + image, *gk = static_cast<const T *>(a.k) + image;
-    const T *gv = static_cast<const T *>(a.v) + image, *gd = static_cast<const T *>(a.dout) + image;
+    const float *gq = static_cast<const float *>(a.q) + image, *gk = static_cast<const float *>(a.k) + image;
+    const float *gv = static_cast<const float *>(a.v) + image, *gd = static_cast<const float *>(a.dout) + image;
     const float4 *stats = a.stats + ((int64_t)it.b * a.heads + it.h) * a.N;
     const int region = region_at(a, it.r);
     const int32_t *start = a.start + (int64_t)it.b * (a.R + 1) + it.r;
@@ -404,8 +394,8 @@ __global__ void __launch_bounds__(32 * WARPS) diff_backward_keys_simt_kernel(con
         const int row = e / nvec, tok = it.t * ROWS + row;
         const bool in = tok < a.rs;
         const int64_t off = (int64_t)(in ? token_at(a, region, tok) : 0) * a.C;
-        stage_vector<T>(sk, hd, row, e % nvec, gk + off, in);
-        stage_vector<T>(sv, hd, row, e % nvec, gv + off, in);
+        stage_vector(sk, hd, row, e % nvec, gk + off, in);
+        stage_vector(sv, hd, row, e % nvec, gv + off, in);
     }
     const float *krows = sk + warp * RW * stride, *vrows = sv + warp * RW * stride;
     const bool busy = it.t * ROWS + warp * RW < a.rs;
@@ -419,8 +409,8 @@ __global__ void __launch_bounds__(32 * WARPS) diff_backward_keys_simt_kernel(con
             const int row = e / nvec, query = q0 + row;
             const bool real = query < nq;
             const int64_t off = real ? (int64_t)query_at(query) * a.C : 0;
-            stage_vector<T>(sq, hd, row, e % nvec, gq + off, real);
-            stage_vector<T>(sd, hd, row, e % nvec, gd + off, real);
+            stage_vector(sq, hd, row, e % nvec, gq + off, real);
+            stage_vector(sd, hd, row, e % nvec, gd + off, real);
         }
         __syncthreads();
         if (!busy) continue;
@@ -465,8 +455,8 @@ __global__ void __launch_bounds__(32 * WARPS) diff_backward_keys_simt_kernel(con
         for (int cc = 0; cc < NC; ++cc) {
             const int c = lane + 32 * cc;
             if (c < hd) {
-                static_cast<T *>(a.dk)[off + c] = from_float<T>(dk[i][cc] * (c < a.d ? w1 : w2));
-                static_cast<T *>(a.dv)[off + c] = from_float<T>(dv[i][cc]);
+                static_cast<float *>(a.dk)[off + c] = (dk[i][cc] * (c < a.d ? w1 : w2));
+                static_cast<float *>(a.dv)[off + c] = (dv[i][cc]);
             }
         }
     }
@@ -482,7 +472,7 @@ cudaError_t launch_with(int grid, int threads, size_t smem, const DiffArgs &a, c
     return launch_pdl(Kernel, dim3(grid), dim3(threads), smem, stream, a);
 }
 
-template <typename T, int WARPS, int RW, int NC> cudaError_t launch_one(DiffArgs &a, bool backward, cudaStream_t stream)
+template <int WARPS, int RW, int NC> cudaError_t launch_one(DiffArgs &a, bool backward, cudaStream_t stream)
 {
     using L = SimtTile<WARPS, RW>;
     a.tiles = (a.rs + L::kRows - 1) / L::kRows;
@@ -494,41 +484,36 @@ template <typename T, int WARPS, int RW, int NC> cudaError_t launch_one(DiffArgs
     const size_t tail = 16 + (((size_t)a.topk * 4 + 15) & ~(size_t)15);
     const int grid = (int)items;
     if (!backward)
-        return launch_with<diff_attend_simt_kernel<T, WARPS, RW, NC>>(grid, 32 * WARPS, 4 * L::floats(a.hd, 1, 2) + tail, a,
+        return launch_with<diff_attend_simt_kernel<WARPS, RW, NC>>(grid, 32 * WARPS, 4 * L::floats(a.hd, 1, 2) + tail, a,
                            stream);
-    const cudaError_t e = launch_with<diff_backward_queries_simt_kernel<T, WARPS, RW, NC>>(grid, 32 * WARPS,
+    const cudaError_t e = launch_with<diff_backward_queries_simt_kernel<WARPS, RW, NC>>(grid, 32 * WARPS,
                                       4 * L::floats(a.hd, 2, 2) + tail, a, stream);
     if (e != cudaSuccess) return e;
-    return launch_with<diff_backward_keys_simt_kernel<T, WARPS, RW, NC>>(grid > a.heads ? grid : a.heads, 32 * WARPS,
+    return launch_with<diff_backward_keys_simt_kernel<WARPS, RW, NC>>(grid > a.heads ? grid : a.heads, 32 * WARPS,
                        4 * L::floats(a.hd, 2, 3), a, stream);
 }
 
-template <typename T, int NC> cudaError_t launch_nc(DiffArgs &a, bool backward, cudaStream_t stream)
+template <int NC> cudaError_t launch_nc(DiffArgs &a, bool backward, cudaStream_t stream)
 {
-    if (a.rs <= 4) return launch_one<T, 4, 1, NC>(a, backward, stream);
-    if (a.rs <= 16) return launch_one<T, 4, 4, NC>(a, backward, stream);
+    if (a.rs <= 4) return launch_one<4, 1, NC>(a, backward, stream);
+    if (a.rs <= 16) return launch_one<4, 4, NC>(a, backward, stream);
     // CTAs of 32 rows: eight to a warp, whose reads feed the most FMAs, or, for many keys, twice the warps of four rows (3
     // regions of 63 tokens, 48 channels: 47 and 53 us; one of 1024, 64 channels: 148 and 112 us)
-    if (diff_simt_warps(a.topk, a.rs) == 4) return launch_one<T, 4, 8, NC>(a, backward, stream);
-    return launch_one<T, 8, 4, NC>(a, backward, stream);
-}
-
-template <typename T> cudaError_t launch_t(DiffArgs &a, bool backward, cudaStream_t stream)
-{
-    switch ((a.hd + 31) / 32) {
-    case 1: return launch_nc<T, 1>(a, backward, stream);
-    case 2: return launch_nc<T, 2>(a, backward, stream);
-    case 3: return launch_nc<T, 3>(a, backward, stream);
-    default: return launch_nc<T, 4>(a, backward, stream);
-    }
+    if (diff_simt_warps(a.topk, a.rs) == 4) return launch_one<4, 8, NC>(a, backward, stream);
+    return launch_one<8, 4, NC>(a, backward, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_diff_simt(const DiffArgs &args, bool backward, bool bf16, cudaStream_t stream)
+cudaError_t launch_diff_simt(const DiffArgs &args, bool backward, cudaStream_t stream)
 {
     DiffArgs a = args;
-    return bf16 ? launch_t<__nv_bfloat16>(a, backward, stream) : launch_t<float>(a, backward, stream);
+    switch ((a.hd + 31) / 32) {
+    case 1: return launch_nc<1>(a, backward, stream);
+    case 2: return launch_nc<2>(a, backward, stream);
+    case 3: return launch_nc<3>(a, backward, stream);
+    default: return launch_nc<4>(a, backward, stream);
+    }
 }
 
 }  // namespace bra

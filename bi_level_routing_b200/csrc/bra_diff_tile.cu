@@ -59,7 +59,6 @@ __global__ void __launch_bounds__(32 * kWarps, DK <= 32 ? 4 : 3) diff_attend_til
     const int item = blockIdx.x * L::kGroups + group;
     if (item >= a.nitems) return;  // the whole group: its barriers are its own
     DiffItem it = diff_item(a, item);  // DENSE: the launcher counts one region and one tile
-    const int dc = a.d / 8;
     const int64_t image = (int64_t)it.b * a.N * a.C + it.h * a.hd;
     const __nv_bfloat16 *gk = static_cast<const __nv_bfloat16 *>(a.k) + image;
     const __nv_bfloat16 *gv = static_cast<const __nv_bfloat16 *>(a.v) + image;
@@ -67,12 +66,6 @@ __global__ void __launch_bounds__(32 * kWarps, DK <= 32 ? 4 : 3) diff_attend_til
     const int tok0 = (DENSE ? 0 : it.t * 16 * WPI) + 16 * wg;
     const int ntok = DENSE ? a.N : a.rs;
     auto token = [&](int tok) { return DENSE ? tok : token_at(a, region, tok); };
-    if (a.d < DK) {  // channels between d and DK multiply zeros
-        for (int e = gtid; e < KT * (HP / 8); e += 32 * WPI) {
-            const int c = e % (HP / 8);
-            if (c % (DK / 8) >= dc) *reinterpret_cast<uint4 *>(sk + (e / (HP / 8)) * ROW + 8 * c) = make_uint4(0, 0, 0, 0);
-        }
-    }
     if (DENSE)
         for (int e = gtid; e < 64 * 16 + 2; e += 32 * WPI) pairs[e] = 0u;
     grid_dependency_wait();
@@ -89,7 +82,7 @@ __global__ void __launch_bounds__(32 * kWarps, DK <= 32 ? 4 : 3) diff_attend_til
         nkeys = *count * a.rs;
     }
     {
-        const int j = lane % L::kLanes, jk = j < dc ? j : DK / 8 + j - dc, r0 = wg * (KT / WPI);
+        const int j = lane % L::kLanes, r0 = wg * (KT / WPI);
         warp_rows<KT / WPI, L::kLanes>(
             lane,
             [&](int row) {
@@ -100,10 +93,10 @@ __global__ void __launch_bounds__(32 * kWarps, DK <= 32 ? 4 : 3) diff_attend_til
                 return token_at(a, bases[slot], tok);
             },
             [&](int row, int at) {
-                if (j >= 2 * dc) return;
-                const int64_t off = (int64_t)max(at, 0) * a.C + 8 * j;
-                cp_async16_or_zero(smem_u32(sk + (r0 + row) * ROW + 8 * jk), gk + off, at >= 0);
-                cp_async16_or_zero(smem_u32(sv + (r0 + row) * ROW + 8 * j), gv + off, at >= 0);
+                if (j >= HP / 8) return;
+                const int64_t off = (int64_t)max(at, 0) * a.C;
+                copy_split<DK>(smem_u32(sk + (r0 + row) * ROW), gk + off, j, a.d, at >= 0);
+                copy_run(smem_u32(sv + (r0 + row) * ROW), gv + off, j, a.hd, at >= 0);
             });
         cp_async_commit();
     }
@@ -167,7 +160,7 @@ __global__ void __launch_bounds__(32 * kWarps, DK <= 32 ? 4 : 3) diff_attend_til
         // and NaN must not: they are taken out of the tile here and put back, below, for the queries that name them.
         for (int e = gtid; e < KT * (HP / 8); e += 32 * WPI) {
             const int key = e / (HP / 8), c = e % (HP / 8);
-            if (c >= 2 * dc) continue;
+            if (8 * c >= a.hd) continue;
             uint4 *at = reinterpret_cast<uint4 *>(sv + key * ROW + 8 * c);
             uint32_t x[4] = {at->x, at->y, at->z, at->w};
             uint32_t found = 0;
@@ -302,7 +295,7 @@ __global__ void __launch_bounds__(32 * kWarps, DK <= 32 ? 4 : 3) diff_attend_til
     }
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + image;
     const int j = lane % L::kLanes;
-    if (j < 2 * dc)
+    if (8 * j < a.hd)
         for (int row = lane / L::kLanes; row < 16; row += 32 / L::kLanes) {
             const int tok = tok0 + row;
             if (tok < ntok)
@@ -311,10 +304,7 @@ __global__ void __launch_bounds__(32 * kWarps, DK <= 32 ? 4 : 3) diff_attend_til
         }
 }
 
-bool diff_tile_supports(const Geometry &g)
-{
-    return diff_mma_supports(g) && (long long)g.topk * g.rs <= kTileKeys;
-}
+bool diff_tile_supports(const Geometry &g) { return (long long)g.topk * g.rs <= kTileKeys; }
 
 namespace {
 

@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, KT == 32 ? 2 : 1) diff_attend_umma_k
 // region of 64 tokens (64 images of 49 regions) 64 against 48.
 bool diff_umma_supports(const Geometry &g)
 {
-    return diff_mma_supports(g) && (g.rs > 64 || (g.rs == 64 && g.topk >= 4));
+    return g.hd % 16 == 0 && (g.rs > 64 || (g.rs == 64 && g.topk >= 4));
 }
 
 namespace {

@@ -206,19 +206,18 @@ struct DiffArgs;  // bra_diff.cuh
 
 // Fills what the kernels need besides the pointers of one call. hd even, at most 128.
 void diff_plan(DiffArgs &a, const Geometry &g);
-// The bf16 tensor-core kernels: hd a multiple of 16 up to 128. The CUDA-core ones: a multiple of 8.
-bool diff_mma_supports(const Geometry &g);
-// The forward kernel for at most 64 keys a query (bf16, the same heads).
+// bf16 maps: mma.sync kernels. fp32 maps: CUDA cores. Heads of a multiple of 8 channels, at most 128.
+cudaError_t launch_diff_attend_mma(const DiffArgs &a, cudaStream_t stream);
+// The forward kernel for at most 64 keys a query (bf16).
 bool diff_tile_supports(const Geometry &g);
 cudaError_t launch_diff_attend_tile(const DiffArgs &a, cudaStream_t stream);
-// The tcgen05 ones (bf16, the same heads): large regions.
+// The tcgen05 ones (bf16, hd a multiple of 16): large regions.
 bool diff_umma_supports(const Geometry &g);
 cudaError_t launch_diff_attend_umma(const DiffArgs &a, cudaStream_t stream);
 bool diff_backward_umma_supports(const Geometry &g);
 cudaError_t launch_diff_backward_umma(const DiffArgs &a, cudaStream_t stream);
-cudaError_t launch_diff_attend_mma(const DiffArgs &a, cudaStream_t stream);
 cudaError_t launch_diff_backward_mma(const DiffArgs &a, cudaStream_t stream);
-cudaError_t launch_diff_simt(const DiffArgs &a, bool backward, bool bf16, cudaStream_t stream);
+cudaError_t launch_diff_simt(const DiffArgs &a, bool backward, cudaStream_t stream);
 // list [B, R * topk] and start [B, R + 1]: for each region the regions that route to it, in order.
 cudaError_t launch_diff_invert(const DiffArgs &a, int32_t *list, int32_t *start, cudaStream_t stream);
 // Partial sums that a family of backward kernels leaves for each head's dlam.

@@ -205,9 +205,9 @@ bra_status bra_attend_backward(const void *q, const void *k, const void *v, cons
      out = (softmax(s q1 k1^T) - lambda[j] softmax(s q2 k2^T)) v,   s = (hd/2)^-1/2.
    n_win = 1 with topk = 1 attends over the whole map. lambda: device fp32 [heads] (the learned weight
    itself; how a model forms it is the caller's); out shares no memory with q, k or v; other arguments, the treatment of idx and the empty
-   row (out = 0) as bra_attend. bf16 with hd a multiple of 16 runs on the tensor cores (P rounded to
-   bf16 for the product with v, everything else fp32), the rest on CUDA cores in fp32; neither
-   depends on bra_set_attend_kernel. BRA_ERR_UNSUPPORTED: hd % 8 != 0, hd > 128 (the limit on
+   row (out = 0) as bra_attend. bf16 runs on the tensor cores (P rounded to bf16 for the
+   product with v, everything else fp32), fp32 on CUDA cores; neither depends on
+   bra_set_attend_kernel. BRA_ERR_UNSUPPORTED: hd % 8 != 0, hd > 128 (the limit on
    a region's row segment, W / n_win * C, holds for routing only). */
 bra_status bra_diff_attend(const void *q, const void *k, const void *v, const int32_t *idx, const float *lambda, void *out,
                            int B, int H, int W, int C, int heads, int n_win, int topk, bra_dtype dtype, void *stream);
