@@ -14,8 +14,13 @@
 //           the launch's first `heads` CTAs also add up dlam from the partial sums.
 //
 // Precision: S and dP are exact products of bf16 in fp32 sums, statistics and accumulators are
-// fp32. P and, for dk, dS enter the last products as bf16. A row's dS sum to 0, so its roundings meet all of k, of which dq keeps
-// only what differs between keys: for dq, dS is two bf16 terms. Each gradient is rounded to bf16 once.
+// fp32. P and, for dk, dS enter the last products as bf16. A row's dS sum to 0, so its roundings meet all of k,
+// of which dq keeps only what differs between keys: for dq, dS is two bf16 terms. Each gradient is rounded
+// to bf16 once.
+//
+// Few warps and the latency of their gathers bound it: three kernels of 168 registers a thread, 12 warps an SM.
+// 64 images of 28 x 28, 2 heads of 64, 4 regions of 16 tokens to a query: 88 us, of which the queries kernel
+// takes 40, the keys kernel 43 and the lists 4; with 8 regions 182 us.
 #include "bra_diff.cuh"
 
 namespace bra {

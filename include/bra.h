@@ -204,11 +204,11 @@ bra_status bra_attend_backward(const void *q, const void *k, const void *v, cons
    the tokens of regions idx[b, r, 0..topk-1],
      out = (softmax(s q1 k1^T) - lambda[j] softmax(s q2 k2^T)) v,   s = (hd/2)^-1/2.
    n_win = 1 with topk = 1 attends over the whole map. lambda: device fp32 [heads] (the learned weight
-   itself; how a model forms it is the caller's); out shares no memory with q, k or v; other arguments, the treatment of idx and the empty
-   row (out = 0) as bra_attend. bf16 runs on the tensor cores (P rounded to bf16 for the
-   product with v, everything else fp32), fp32 on CUDA cores; neither depends on
-   bra_set_attend_kernel. BRA_ERR_UNSUPPORTED: hd % 8 != 0, hd > 128 (the limit on
-   a region's row segment, W / n_win * C, holds for routing only). */
+   itself; how a model forms it is the caller's); out shares no memory with q, k or v; other arguments, the
+   treatment of idx and the empty row (out = 0) as bra_attend. bf16 runs on the tensor cores (P rounded to
+   bf16 for the product with v, everything else fp32), fp32 on CUDA cores; neither depends on
+   bra_set_attend_kernel. BRA_ERR_UNSUPPORTED: hd % 8 != 0, hd > 128 (the limit on a region's row segment,
+   W / n_win * C, holds for routing only). */
 bra_status bra_diff_attend(const void *q, const void *k, const void *v, const int32_t *idx, const float *lambda, void *out,
                            int B, int H, int W, int C, int heads, int n_win, int topk, bra_dtype dtype, void *stream);
 
@@ -220,9 +220,9 @@ bra_status bra_forward_diff(const void *q, const void *k, const void *v, int32_t
 /* Backward of bra_diff_attend with the routing index held fixed: the gradients of sum(dout * out) by
    q, k, v and lambda. dq, dk, dv: device [B, H, W, C] of dtype, written (regions that nothing routes to
    get 0): each element is summed in fp32 inside one CTA and rounded once, so the gradients are the same
-   bits on every run and nothing wider would be gained; they share no memory with each other or the inputs. dlambda: device
-   fp32 [heads], written (0 for B == 0). Takes scratch from the pool: 16 bytes for each (token, head), and
-   the index sorted by routed region. BRA_ERR_UNSUPPORTED: as bra_diff_attend, or
+   bits on every run and nothing wider would be gained; they share no memory with each other or the
+   inputs. dlambda: device fp32 [heads], written (0 for B == 0). Takes scratch from the pool: 16 bytes for
+   each (token, head), and the index sorted by routed region. BRA_ERR_UNSUPPORTED: as bra_diff_attend, or
    H * W * topk > 2^30. */
 bra_status bra_diff_attend_backward(const void *q, const void *k, const void *v, const int32_t *idx, const float *lambda,
                                     const void *dout, void *dq, void *dk, void *dv, float *dlambda, int B, int H, int W,
