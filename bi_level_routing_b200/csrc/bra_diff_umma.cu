@@ -2,7 +2,7 @@
 // (tcgen05, TMEM accumulators), for heads of 16 to 128 channels in multiples of 16 and large regions (see
 // bra_diff.cuh for the formula). Heads are padded with zeros to 64 or 128 channels. Two exponentials a query-key pair against 6 hd
 // tensor operations: the exponential unit (16 a cycle and SM) is the bound, 1024 cycles for 128 queries and 64
-// keys; 16384-token maps (2 images, 2 heads of 64) take 749 us, 1.25 times that at the clock they run at.
+// keys; 16384-token maps (2 images, 2 heads of 64) take 749 us, of which that unit's share is 390.
 //
 // A CTA owns 128 query tokens of one (image, region, head) and meets the routed keys in tiles of KT: 32 for heads
 // of up to 64 channels, whose accumulators leave room in TMEM for two CTAs on an SM (four softmax warps a
