@@ -698,6 +698,13 @@ static bool overlaps(const void *p, const void *r, size_t bytes)
 // Whether two buffers of `bytes` share memory at all.
 static bool shares(const void *p, const void *r, size_t bytes) { return p == r || overlaps(p, r, bytes); }
 
+// Whether [p, p + np) and [r, r + nr) share memory.
+static bool meet(const void *p, size_t np, const void *r, size_t nr)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(r);
+    return x < y ? y - x < np : x - y < nr;
+}
+
 // The sizes both passes take: heads of a multiple of 8 channels, at most 128.
 static bra_status check_diff(int B, int H, int W, int C, int heads, int n_win, int topk, bra_dtype dtype, bool routes,
                              bra::Geometry *g)
@@ -790,6 +797,7 @@ bra_status bra_diff_attend_backward(const void *q, const void *k, const void *v,
             if (shares(outs[i], in, bytes)) return BRA_ERR_INVALID_ARG;
         if (shares(outs[i], outs[(i + 1) % 3], bytes)) return BRA_ERR_INVALID_ARG;
     }
+    if (shares(dlambda, lambda, (size_t)heads * sizeof(float))) return BRA_ERR_INVALID_ARG;
     // the queries that meet one region are numbered in 31 bits
     if ((long long)g.N * topk > (1LL << 30)) return BRA_ERR_UNSUPPORTED;
     DeviceState *st = nullptr;
@@ -898,15 +906,15 @@ static bra_status norm_args(bra::NormArgs *a, const void *x, const void *h, cons
     if (B < 0 || H <= 0 || W <= 0 || C <= 0 || (kind != BRA_NORM_LAYER && kind != BRA_NORM_RMS)) return BRA_ERR_INVALID_ARG;
     if (!(eps >= 0.f)) return BRA_ERR_INVALID_ARG;
     if (((long long)C * (dtype == BRA_BF16 ? 2 : 4)) % 16 != 0) return BRA_ERR_INVALID_ARG;
-    if (!h && (gate || post_w)) return BRA_ERR_INVALID_ARG;          // nothing to gate or normalise
     if ((!post_w && post_b) || (!pre_w && pre_b)) return BRA_ERR_INVALID_ARG;  // a bias belongs to its weight
-    if (!h && !pre_w) return BRA_ERR_INVALID_ARG;                     // nothing to do
     if (gate ? (gate_images != 1 && gate_images != B) : gate_images != 0) return BRA_ERR_INVALID_ARG;
     if (!bra::norm_supports(C, dtype == BRA_BF16)) return BRA_ERR_UNSUPPORTED;
     const long long rows = (long long)H * W;
     const bool own = gate && gate_images > 1;
     if (rows > 0x7fffffffLL / 2 || (!own && rows * B > 0x7fffffffLL / 2)) return BRA_ERR_UNSUPPORTED;
-    if (B == 0) return BRA_OK;
+    if (B == 0) return BRA_OK;  // the maps hold nothing and may be NULL
+    if (!h && (gate || post_w)) return BRA_ERR_INVALID_ARG;  // nothing to gate or normalise
+    if (!h && !pre_w) return BRA_ERR_INVALID_ARG;            // nothing to do
     if (!x || !aligned(x, 16) || !aligned(h, 16) || !aligned(gate, 16) || !aligned(post_w, 16) || !aligned(post_b, 16) ||
         !aligned(pre_w, 16) || !aligned(pre_b, 16))
         return BRA_ERR_INVALID_ARG;
@@ -983,6 +991,17 @@ bra_status bra_norm_residual_backward(const void *x, const void *h, const void *
         for (const void *in : {x, h, dy, ds})
             if (out && in && overlaps(out, in, bytes)) return BRA_ERR_INVALID_ARG;
     if (dh && (dx == dh || overlaps(dx, dh, bytes))) return BRA_ERR_INVALID_ARG;
+    // the weights' gradients are written by many CTAs while others still read the weights
+    const size_t row = (size_t)C * sizeof(float), rows = gate_images * row;
+    const struct { const void *p; size_t bytes; } read[] = {{gate, rows}, {post_weight, row}, {post_bias, row}, {pre_weight, row},
+                                                            {pre_bias, row}},
+        written[] = {{dgate, rows}, {dpost_weight, row}, {dpost_bias, row}, {dpre_weight, row}, {dpre_bias, row}};
+    for (int i = 0; i < 5; ++i)
+        for (int j = 0; j < 5 && written[i].p; ++j) {
+            if (read[j].p && meet(written[i].p, written[i].bytes, read[j].p, read[j].bytes)) return BRA_ERR_INVALID_ARG;
+            if (j < i && written[j].p && meet(written[i].p, written[i].bytes, written[j].p, written[j].bytes))
+                return BRA_ERR_INVALID_ARG;
+        }
     DeviceState *st = nullptr;
     if ((s = device_state(&st)) != BRA_OK) return s;
     a.dy = dy;
@@ -1066,13 +1085,18 @@ int bra_kernels_per_call(const char *entry_point, int B, int H, int W, int C, in
 {
     if (!entry_point || B <= 0) return 0;
     bra::Geometry g;
-    if (check_shape(B, H, W, C, heads, n_win, topk, dtype, &g) != BRA_OK) return 0;
+    const bool routes = std::strncmp(entry_point, "bra_diff_", 9) && (n_win != 1 || std::strcmp(entry_point, "bra_forward_diff"));
+    if (check_shape(B, H, W, C, heads, n_win, topk, dtype, &g, routes) != BRA_OK) return 0;
     const int route = (g.rs == 1 && g.R <= 256) ? 1 : 2;
     const int attend = choose_attend_kernel(g, dtype) < 0 ? 0 : 1;
     if (!std::strcmp(entry_point, "bra_route")) return route;
     if (!std::strcmp(entry_point, "bra_attend")) return attend;
     if (!std::strcmp(entry_point, "bra_forward") || !std::strcmp(entry_point, "bra_forward_host"))
         return attend ? (fused_forward(g, dtype) ? 1 : route + attend) : 0;
+    if (g.hd % 8 != 0 || g.hd > 128) return 0;
+    if (!std::strcmp(entry_point, "bra_diff_attend")) return 1;
+    if (!std::strcmp(entry_point, "bra_forward_diff")) return g.R == 1 ? 1 : route + 1;
+    if (!std::strcmp(entry_point, "bra_diff_attend_backward")) return (long long)g.N * topk > (1LL << 30) ? 0 : 3;
     return 0;
 }
 

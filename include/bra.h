@@ -221,7 +221,7 @@ bra_status bra_forward_diff(const void *q, const void *k, const void *v, int32_t
    q, k, v and lambda. dq, dk, dv: device [B, H, W, C] of dtype, written (regions that nothing routes to
    get 0): each element is summed in fp32 inside one CTA and rounded once, so the gradients are the same
    bits on every run and nothing wider would be gained; they share no memory with each other or the
-   inputs. dlambda: device fp32 [heads], written (0 for B == 0). Takes scratch from the pool: 16 bytes for
+   inputs. dlambda: device fp32 [heads], written (0 for B == 0), not lambda itself. Takes scratch from the pool: 16 bytes for
    each (token, head), and the index sorted by routed region. BRA_ERR_UNSUPPORTED: as bra_diff_attend, or
    H * W * topk > 2^30. */
 bra_status bra_diff_attend_backward(const void *q, const void *k, const void *v, const int32_t *idx, const float *lambda,
@@ -261,8 +261,9 @@ bra_status bra_norm_residual(const void *x, const void *h, const float *gate, in
 /* Backward of bra_norm_residual from its inputs: the gradients of sum(ds * s) + sum(dy * y). dy is given
    exactly where pre_weight is; ds NULL counts as 0 (one of the two is given). dx and, where h is given,
    dh: device [B, H, W, C] of dtype, written; distinct, and may be one of x, h, dy, ds themselves. The weights'
-   gradients (device fp32, of their weights' shapes; each given exactly where its weight is) are summed in a
-   fixed order, the same bits on every run; for B == 0 they are 0. Takes scratch from the pool: 16 C
+   gradients (device fp32, of their weights' shapes; each given exactly where its weight is; they share no
+   memory with each other or a weight) are summed in a fixed order, the same bits on every run; for B == 0
+   they are 0. Takes scratch from the pool: 16 C
    bytes for each CTA of the launch. */
 bra_status bra_norm_residual_backward(const void *x, const void *h, const void *dy, const void *ds, const float *gate,
                                       int gate_images, const float *post_weight, const float *post_bias,
@@ -311,7 +312,7 @@ bra_status bra_check_device_error(void *stream);
 size_t bra_route_scratch_bytes(int B, int H, int W, int C, int n_win);
 
 /* Number of library kernels one call of `entry_point` ("bra_route", "bra_attend",
-   "bra_forward", "bra_forward_host") launches with these arguments, for launch accounting
+   "bra_forward", "bra_forward_host", "bra_diff_attend", "bra_forward_diff", "bra_diff_attend_backward") launches with these arguments, for launch accounting
    (memset and copy nodes not counted); 0 for a call that would launch nothing or be rejected. */
 int bra_kernels_per_call(const char *entry_point, int B, int H, int W, int C, int heads, int n_win, int topk,
                          bra_dtype dtype);

@@ -162,3 +162,26 @@ def test_norm_rejects(L):
     for kw in (dict(dx=0), dict(dh=0), dict(dy=0), dict(dg=0), dict(dpw=0), dict(dpb=0), dict(dnw=0), dict(dnb=0), dict(h=0), dict(pb=0),
                dict(dx=A[10]), dict(dx=A[0] + 16), dict(dh=A[2] + 16), dict(dg=A[11] + 2), dict(nw=0, nb=0, dnw=0, dnb=0, dy=0, ds=0)):
         assert back(**kw) == INVALID, kw
+
+    # weight gradients over a weight, over each other, or a part of one
+    for kw in (dict(dg=A[4]), dict(dg=A[4] + 64 * 4), dict(dpw=A[5]), dict(dpb=A[5] + 16), dict(dnw=A[8]), dict(dnb=A[14]), dict(dpw=A[11] + 256)):
+        assert back(**kw) == INVALID, kw
+
+
+def test_dlambda_over_lambda(L):
+    apart = [P + (i << 24) for i in range(10)]
+    for shift in (0, 4):  # two heads: eight bytes
+        p = list(apart)
+        p[9] = p[4] + shift
+        assert L.bra_diff_attend_backward(*p, *_sizes({}), None) == INVALID
+
+
+def test_kernels_per_call(L):
+    stage1 = (64, 56, 56, 64, 1, 7, 1, 1)
+    assert L.bra_kernels_per_call(b"bra_diff_attend", *stage1) == 1
+    assert L.bra_kernels_per_call(b"bra_forward_diff", *stage1) == 3  # means, affinity and top-k, attention
+    assert L.bra_kernels_per_call(b"bra_diff_attend_backward", *stage1) == 3  # index by region, queries, keys
+    whole = (1, 64, 4096, 64, 1, 1, 1, 1)  # one region: nothing is routed, and its rows may be of any length
+    assert L.bra_kernels_per_call(b"bra_forward_diff", *whole) == 1
+    assert L.bra_kernels_per_call(b"bra_forward", *whole) == 0
+    assert L.bra_kernels_per_call(b"bra_diff_attend", 64, 56, 56, 64, 16, 7, 1, 1) == 0  # heads of 4 channels

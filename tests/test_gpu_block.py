@@ -315,3 +315,114 @@ def test_block_and_its_gradients(captured):
                        ("post weight", dn2, n26.grad), ("pre weight", dn1, n16.grad)):
         err = float((a.double().cpu() - b).abs().max())
         assert err <= 1e4 * 2.0 ** -24 * max(1.0, float(b.abs().max())), f"{name}: {err}"
+
+
+# ------------------------------------------------------------------ calls at the edges
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_empty_batches(dtype):
+    """No image: empty results, and sums over nothing are 0."""
+    x = torch.empty((0, 6, 6, 64), device="cuda", dtype=dtype)
+    idx = torch.empty((0, 9, 2), device="cuda", dtype=torch.int32)
+    lam, w = torch.ones(2, device="cuda"), torch.ones(64, device="cuda")
+    assert bra.diff_attend(x, x, x, idx, lam, 2, 3).shape == x.shape
+    out, routed = bra.forward_diff(x, x, x, lam, 3, 2, 2)
+    assert out.shape == x.shape and routed.shape == idx.shape
+    grads = bra.diff_attend_backward(x, x, x, idx, lam, x, 2, 3)
+    assert all(t.shape == x.shape for t in grads[:3]) and grads[3].tolist() == [0.0, 0.0]
+    q, k = bra.rope(x, x, torch.ones(4, device="cuda"), 2)
+    assert q.shape == x.shape and k.shape == x.shape
+    for gate in (w, torch.empty((0, 64), device="cuda")):
+        s, y = bra.norm_residual(x, x, gate=gate, post_weight=w, post_bias=w, pre_weight=w)
+        assert s.shape == x.shape and y.shape == x.shape
+        g = bra.norm_residual_backward(x, x, x, x, gate=gate, post_weight=w, post_bias=w, pre_weight=w)
+        assert g.dx.shape == x.shape and g.dh.shape == x.shape and g.dgate.shape == gate.shape
+        assert all(not bool(t.any()) for t in (g.dgate, g.dpost_weight, g.dpost_bias, g.dpre_weight))
+
+
+def test_two_threads():
+    """Two threads, each on a stream of its own, get what they get one after the other."""
+    import threading
+
+    def inputs(seed):
+        q, k, v, d = (randn((3, 20, 20, 64), seed + i, BF16) for i in range(4))
+        idx = torch.randint(0, 4, (3, 4, 2), generator=torch.Generator().manual_seed(seed), dtype=torch.int32).cuda()
+        return q, k, v, d, idx, randn((2,), seed + 5), randn((64,), seed + 6)
+
+    freqs, _ = bra.rope_frequencies(4, device="cuda")
+
+    def work(q, k, v, d, idx, lam, w):
+        q, k = bra.rope(q, k, freqs, 4)
+        out = bra.diff_attend(q, k, v, idx, lam, 2, 2)
+        s, y = bra.norm_residual(v, out, gate=w, post_weight=w, pre_weight=w)
+        n = bra.norm_residual_backward(v, out, d, None, gate=w, post_weight=w, pre_weight=w)
+        return [s, y, *(t for t in n if t is not None), *bra.diff_attend_backward(q, k, v, idx, lam, n.dh, 2, 2)]
+
+    sets = [inputs(300), inputs(400)]
+    want = [work(*s) for s in sets]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(30):
+                    got = work(*sets[i])
+                    stream.synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                        wrong.append(i)
+        except Exception as e:  # noqa: BLE001  (reported below: a thread's exception ends nothing)
+            wrong.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+# (elements just above 2^32 in bf16, above 2^31 in fp32) regions of 1024, 64 and 4 tokens; 64-token regions, two routed
+FAR = [(33, 1024, 128, 32, 1, BF16), (2080, 128, 128, 16, 1, BF16), (2080, 128, 128, 16, 2, BF16), (33000, 32, 128, 16, 3, BF16),
+       (1050, 128, 128, 16, 1, F32)]
+
+
+@pytest.mark.parametrize("B,H,C,n_win,topk,dtype", FAR, ids=lambda v: str(v).removeprefix("torch."))
+def test_offsets_past_32_bits(B, H, C, n_win, topk, dtype):
+    """The last images of arrays whose offsets pass 32 bits are those of a call on these images alone, bit for bit."""
+    assert B * H * H * C > (2 ** 32 if dtype is BF16 else 2 ** 31)
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 70e9:
+        pytest.skip("needs 70 GB of device memory")
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.empty((B, H, H, C), device="cuda", dtype=dtype)
+    for part in x.split(max(1, B // 16)):
+        part.normal_(generator=gen)
+    R = n_win * n_win
+    idx = torch.randint(0, R, (B, R, topk), generator=gen, device="cuda", dtype=torch.int32)
+    lam, w = torch.full((1,), 0.3, device="cuda"), torch.rand(C, generator=gen, device="cuda")
+    tail = x[-2:].clone()
+    last = idx[-2:].contiguous()
+    same = lambda far, near: torch.equal(far[-2:], near)
+    far = bra.diff_attend(x, x, x, idx, lam, 1, n_win)
+    assert same(far, bra.diff_attend(tail, tail, tail, last, lam, 1, n_win))
+    del far
+    far = bra.diff_attend_backward(x, x, x, idx, lam, x, 1, n_win)
+    near = bra.diff_attend_backward(tail, tail, tail, last, lam, tail, 1, n_win)
+    assert all(same(a, b) for a, b in zip(far[:3], near[:3]))
+    del far
+    freqs, _ = bra.rope_frequencies(16, device="cuda")
+    far = bra.rope(x, None, freqs, 2)[0]
+    assert same(far, bra.rope(tail, None, freqs, 2)[0])
+    del far
+    s, y = bra.norm_residual(x, x, gate=w, post_weight=w, pre_weight=w)
+    near = bra.norm_residual(tail, tail, gate=w, post_weight=w, pre_weight=w)
+    assert same(s, near[0]) and same(y, near[1])
+    del s, y
+    far = bra.norm_residual_backward(x, x, x, x, gate=w, post_weight=w, pre_weight=w)
+    near = bra.norm_residual_backward(tail, tail, tail, tail, gate=w, post_weight=w, pre_weight=w)
+    assert same(far.dx, near.dx) and same(far.dh, near.dh)
+    assert bra.check_device_error() == 0
+    del far
+    torch.cuda.empty_cache()
