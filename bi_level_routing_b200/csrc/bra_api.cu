@@ -731,10 +731,31 @@ static bra_status diff_attend_impl(const void *q, const void *k, const void *v, 
     a.lam = lambda;
     a.out = out;
     a.err = st->error_word;
-    const cudaError_t e = dtype != BRA_BF16            ? bra::launch_diff_simt(a, false, stream)
-                          : bra::diff_tile_supports(g) ? bra::launch_diff_attend_tile(a, stream)
-                          : bra::diff_umma_supports(g) ? bra::launch_diff_attend_umma(a, stream)
-                                                       : bra::launch_diff_attend_mma(a, stream);
+    cudaError_t e;
+    if (dtype != BRA_BF16) {
+        e = bra::launch_diff_simt(a, false, stream);
+    } else if (bra::diff_tile_supports(g)) {
+        e = bra::launch_diff_attend_tile(a, stream);
+    } else if (!bra::diff_umma_supports(g)) {
+        e = bra::launch_diff_attend_mma(a, stream);
+    } else {
+        size_t scratch = 0;
+        a.splits = bra::diff_umma_splits(g, st->num_sms, &scratch);
+        void *ws = nullptr;
+        if (a.splits > 1) {
+            e = cudaMallocFromPoolAsync(&ws, scratch, st->pool, stream);
+            if (e != cudaSuccess) return cuda_fail(e, "cudaMallocFromPoolAsync(split keys)");
+            // the maxima and sums, 2 KB a CTA, lie behind the sums of P V
+            const size_t parts = (size_t)g.B * g.R * ((g.rs + 127) / 128) * g.heads * a.splits;
+            a.split_out = static_cast<float4 *>(ws);
+            a.split_stats = reinterpret_cast<float2 *>(static_cast<uint8_t *>(ws) + scratch - parts * 256 * sizeof(float2));
+        }
+        e = bra::launch_diff_attend_umma(a, stream);
+        if (ws) {
+            const cudaError_t f = cudaFreeAsync(ws, stream);
+            if (e == cudaSuccess) e = f;
+        }
+    }
     return e == cudaSuccess ? BRA_OK : cuda_fail(e, "differential attention kernel");
 }
 
@@ -1094,8 +1115,12 @@ int bra_kernels_per_call(const char *entry_point, int B, int H, int W, int C, in
     if (!std::strcmp(entry_point, "bra_forward") || !std::strcmp(entry_point, "bra_forward_host"))
         return attend ? (fused_forward(g, dtype) ? 1 : route + attend) : 0;
     if (g.hd % 8 != 0 || g.hd > 128) return 0;
-    if (!std::strcmp(entry_point, "bra_diff_attend")) return 1;
-    if (!std::strcmp(entry_point, "bra_forward_diff")) return g.R == 1 ? 1 : route + 1;
+    size_t scratch;
+    DeviceState *st = nullptr;
+    const bool split = dtype == BRA_BF16 && !bra::diff_tile_supports(g) && bra::diff_umma_supports(g) &&
+                       bra::diff_umma_splits(g, device_state(&st) == BRA_OK ? st->num_sms : 148, &scratch) > 1;
+    if (!std::strcmp(entry_point, "bra_diff_attend")) return 1 + split;
+    if (!std::strcmp(entry_point, "bra_forward_diff")) return (g.R == 1 ? 1 : route + 1) + split;
     if (!std::strcmp(entry_point, "bra_diff_attend_backward")) return (long long)g.N * topk > (1LL << 30) ? 0 : 3;
     return 0;
 }

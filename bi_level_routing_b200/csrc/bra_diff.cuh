@@ -55,6 +55,11 @@ struct DiffArgs {
     int nitems;     // work items of the launch
     int nparts;
     int num_sms;
+    // the tcgen05 forward pass, an item's keys split over several CTAs
+    int splits, per;       // CTAs of an item, keys of one
+    float4 *split_out;     // [CTA][map][16-byte chunk][128 rows]: sums of P V
+    float2 *split_stats;   // [CTA][map][128 rows]: maximum, sum
+    FastDiv by_splits;
     float scale;        // d^-1/2
     float scale_log2;   // d^-1/2 log2(e)
     FastDiv by_rs, by_wr, by_nwin, by_heads, by_tiles, by_R, by_topk;

@@ -1,8 +1,8 @@
 // bra_diff_umma.cu -- forward differential attention of bf16 maps on the 5th-generation tensor cores
 // (tcgen05, TMEM accumulators), for heads of 16 to 128 channels in multiples of 16 and large regions (see
-// bra_diff.cuh for the formula). Heads are padded with zeros to 64 or 128 channels. Two exponentials a query-key pair against 6 hd
-// tensor operations: the exponential unit (16 a cycle and SM) is the bound, 1024 cycles for 128 queries and 64
-// keys; 16384-token maps (2 images, 2 heads of 64) take 749 us, of which that unit's share is 390.
+// bra_diff.cuh for the formula). Heads are padded with zeros to 64 or 128 channels. Two exponentials a query-key
+// pair against 6 hd tensor operations: the exponential unit (16 a cycle and SM) is the bound, 1024 cycles for 128
+// queries and 64 keys; 16384-token maps (2 images, 2 heads of 64) take 749 us, of which that unit's share is 390.
 //
 // A CTA owns 128 query tokens of one (image, region, head) and meets the routed keys in tiles of KT: 32 for heads
 // of up to 64 channels, whose accumulators leave room in TMEM for two CTAs on an SM (four softmax warps a
@@ -20,6 +20,8 @@
 //    128-byte swizzled; regions of any size pack densely, rows past the last key are zeros. A lane finds
 //    the address of one row, eight lanes copy it. Warp 11 gathers the query rows and hands the
 //    tiles that have landed to warp 8.
+// Where there are too few (query tile, head) pairs for the GPU, SPLIT: several CTAs share one, each with a run of its
+// keys, and leave both maps' sums of P V, maxima and sums, which a second kernel joins.
 // Every wait is bounded (kErrTimeout); no thread leaves before the TMEM is released.
 #include "bra_diff.cuh"
 
@@ -49,7 +51,7 @@ template <int NB, int KT> struct UmmaTile {
 
 }  // namespace
 
-template <int NB, int KT>
+template <int NB, int KT, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, KT == 32 ? 2 : 1) diff_attend_umma_kernel(const DiffArgs a)
 {
     using L = UmmaTile<NB, KT>;
@@ -69,7 +71,9 @@ __global__ void __launch_bounds__(kThreads, KT == 32 ? 2 : 1) diff_attend_umma_k
     int *count = reinterpret_cast<int *>(tmem_slot + 1);
     int *bases = count + 3;
     const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    const DiffItem it = diff_item(a, blockIdx.x);
+    int item = blockIdx.x, split = 0;
+    if (SPLIT) a.by_splits.divmod(blockIdx.x, item, split);
+    const DiffItem it = diff_item(a, item);
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 32);
@@ -99,7 +103,8 @@ __global__ void __launch_bounds__(kThreads, KT == 32 ? 2 : 1) diff_attend_umma_k
     __syncthreads();
     tcgen05_after_sync();
     const uint32_t tmem = *tmem_slot;
-    const int nkeys = *count * a.rs;
+    const int key0 = SPLIT ? split * a.per : 0;  // this CTA's first key
+    const int nkeys = SPLIT ? min(max(*count * a.rs - key0, 0), a.per) : *count * a.rs;
     const int ntiles = (nkeys + KT - 1) / KT;
     const int64_t image = (int64_t)it.b * a.N * a.C + it.h * a.hd;
     const int region = region_at(a, it.r);
@@ -156,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, KT == 32 ? 2 : 1) diff_attend_umma_k
                 int at = -1;
                 if (key < nkeys) {
                     int slot, tok;
-                    a.by_rs.divmod(key, slot, tok);
+                    a.by_rs.divmod(key0 + key, slot, tok);
                     at = token_at(a, bases[slot], tok);
                 }
                 if (!mbar_wait(&kv_empty[st], (uint32_t)(((i / ST) & 1) ^ 1), a.err)) break;
@@ -324,37 +329,60 @@ __global__ void __launch_bounds__(kThreads, KT == 32 ? 2 : 1) diff_attend_umma_k
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[2 * m + (i & 1)]);
         }
-        // out = O1 / l1 - lam O2 / l2: thread `row` of map m's warps writes half m of the row's channels
-        sum[128 * m + row] = mx == -INFINITY ? 0.f : l;  // only -inf scores: the polynomial's least values are not a sum
-        named_barrier(1, 256);
-        for (int x = 0; x < 2 && ntiles > 0 && alive; ++x)  // the commit after the last tile's products
-            alive = mbar_wait(&s_full[2 * x + ((ntiles + 1) & 1)], (uint32_t)(((ntiles + 1) >> 1) & 1), a.err);
-        tcgen05_after_sync();
-        const float l1 = sum[row], l2 = sum[128 + row], lam = __ldg(a.lam + it.h);
-        const float w1 = over_sum(1.f, l1, nkeys > 0), w2 = over_sum(-lam, l2, nkeys > 0);
-        const bool in = tok0 + row < a.rs;
-        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + image + 32 * NB * m;
-        if (in) out += (int64_t)token_at(a, region, tok0 + row) * a.C;
+        if constexpr (SPLIT) {
+            // A sum of -1 is a CTA without keys; scores that are all -inf have a sum of 0 (the polynomial's least values are
+            // not one), or NaN where one was NaN.
+            const int64_t part = 2 * (int64_t)blockIdx.x + m;
+            if (alive && ntiles > 0)
+                alive = mbar_wait(&s_full[2 * m + ((ntiles + 1) & 1)], (uint32_t)(((ntiles + 1) >> 1) & 1), a.err);
+            tcgen05_after_sync();
+            if (alive) a.split_stats[part * 128 + row] = make_float2(mx, ntiles == 0 ? -1.f : mx == -INFINITY && l == l ? 0.f : l);
+            float4 *dst = a.split_out + part * (16 * NB * 128) + row;
 #pragma unroll
-        for (int c = 0; c < NB; ++c) {
-            uint32_t o1[32], o2[32];
-            if (ntiles > 0) {  // the same for the whole CTA: tcgen05.ld is warp-wide
-                tmem_ld_32x32(t_row + 4 * KT + 32 * NB * m + 32 * c, o1);
-                tmem_ld_32x32(t_row + 4 * KT + 64 * NB + 32 * NB * m + 32 * c, o2);
+            for (int c = 0; c < 2 * NB; ++c) {
+                if (ntiles == 0) break;
+                uint32_t o[32];
+                tmem_ld_32x32(t_o + 32 * c, o);
                 tmem_wait_ld();
+                if (!alive) continue;
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    dst[(8 * c + x) * 128] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
+                                                         __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
             }
-            if (!in || !alive) continue;
+        } else {
+            // out = O1 / l1 - lam O2 / l2: thread `row` of map m's warps writes half m of the row's channels
+            sum[128 * m + row] = mx == -INFINITY ? 0.f : l;  // only -inf scores: the polynomial's least values are not a sum
+            named_barrier(1, 256);
+            for (int x = 0; x < 2 && ntiles > 0 && alive; ++x)  // the commit after the last tile's products
+                alive = mbar_wait(&s_full[2 * x + ((ntiles + 1) & 1)], (uint32_t)(((ntiles + 1) >> 1) & 1), a.err);
+            tcgen05_after_sync();
+            const float l1 = sum[row], l2 = sum[128 + row], lam = __ldg(a.lam + it.h);
+            const float w1 = over_sum(1.f, l1, nkeys > 0), w2 = over_sum(-lam, l2, nkeys > 0);
+            const bool in = tok0 + row < a.rs;
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + image + 32 * NB * m;
+            if (in) out += (int64_t)token_at(a, region, tok0 + row) * a.C;
 #pragma unroll
-            for (int x = 0; x < 32; x += 8) {
-                uint32_t pk[4];
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int z = x + 2 * y;
-                    const float u = fmaf(__uint_as_float(o1[z]), w1, __uint_as_float(o2[z]) * w2);
-                    const float w = fmaf(__uint_as_float(o1[z + 1]), w1, __uint_as_float(o2[z + 1]) * w2);
-                    pk[y] = ntiles > 0 ? pack_bf16x2(u, w) : 0u;
+            for (int c = 0; c < NB; ++c) {
+                uint32_t o1[32], o2[32];
+                if (ntiles > 0) {  // the same for the whole CTA: tcgen05.ld is warp-wide
+                    tmem_ld_32x32(t_row + 4 * KT + 32 * NB * m + 32 * c, o1);
+                    tmem_ld_32x32(t_row + 4 * KT + 64 * NB + 32 * NB * m + 32 * c, o2);
+                    tmem_wait_ld();
                 }
-                if (32 * NB * m + 32 * c + x < a.hd) *reinterpret_cast<uint4 *>(out + 32 * c + x) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                if (!in || !alive) continue;
+#pragma unroll
+                for (int x = 0; x < 32; x += 8) {
+                    uint32_t pk[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int z = x + 2 * y;
+                        const float u = fmaf(__uint_as_float(o1[z]), w1, __uint_as_float(o2[z]) * w2);
+                        const float w = fmaf(__uint_as_float(o1[z + 1]), w1, __uint_as_float(o2[z + 1]) * w2);
+                        pk[y] = ntiles > 0 ? pack_bf16x2(u, w) : 0u;
+                    }
+                    if (32 * NB * m + 32 * c + x < a.hd) *reinterpret_cast<uint4 *>(out + 32 * c + x) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                }
             }
         }
     }
@@ -362,6 +390,52 @@ __global__ void __launch_bounds__(kThreads, KT == 32 ? 2 : 1) diff_attend_umma_k
     __syncthreads();
     tcgen05_after_sync();
     if (warp == 8) tmem_dealloc(tmem, kCols);
+}
+
+// A CTA joins 8 channels of an item's 128 rows, a row to a thread: each map's splits relative to the largest of their
+// maxima, then out = O1 / l1 - lam O2 / l2.
+template <int NB> __global__ void __launch_bounds__(128) diff_attend_join_kernel(const DiffArgs a)
+{
+    const int item = blockIdx.x / (a.hd / 8), chunk = blockIdx.x - item * (a.hd / 8);
+    const int row = threadIdx.x;
+    const DiffItem it = diff_item(a, item);
+    grid_dependency_wait();
+    const int tok = it.t * 128 + row;
+    if (tok >= a.rs) return;
+    const float2 *stats = a.split_stats + (int64_t)item * a.splits * 256 + row;
+    const float4 *part = a.split_out + (int64_t)item * a.splits * (2 * 16 * NB * 128) + 2 * chunk * 128 + row;
+    float o[8] = {};
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        float top = -INFINITY, l = 0.f, x[8] = {};
+        bool some = false;
+        for (int s = 0; s < a.splits; ++s) top = fmaxf(top, __ldcg(stats + (2 * s + m) * 128).x);
+#pragma unroll 4
+        for (int s = 0; s < a.splits; ++s) {
+            const float2 st = __ldcg(stats + (2 * s + m) * 128);
+            if (st.y == -1.f) continue;
+            some = true;
+            const float w = st.x == -INFINITY ? 0.f : fast_exp2(st.x - top);
+            l += st.x == -INFINITY ? st.y : st.y * w;
+            const float4 *src = part + (int64_t)(2 * s + m) * (16 * NB * 128);
+            const float4 u = __ldcg(src), v = __ldcg(src + 128);
+            x[0] = fmaf(u.x, w, x[0]);
+            x[1] = fmaf(u.y, w, x[1]);
+            x[2] = fmaf(u.z, w, x[2]);
+            x[3] = fmaf(u.w, w, x[3]);
+            x[4] = fmaf(v.x, w, x[4]);
+            x[5] = fmaf(v.y, w, x[5]);
+            x[6] = fmaf(v.z, w, x[6]);
+            x[7] = fmaf(v.w, w, x[7]);
+        }
+        const float w = over_sum(m ? -__ldg(a.lam + it.h) : 1.f, l, some);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = fmaf(x[i], w, o[i]);
+    }
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + ((int64_t)it.b * a.N + token_at(a, region_at(a, it.r), tok)) * a.C +
+                         it.h * a.hd + 8 * chunk;
+    *reinterpret_cast<uint4 *>(out) =
+        make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
 }
 
 // Any head the register-tiled kernel takes; regions whose query tiles are more than half full, or just
@@ -375,14 +449,47 @@ bool diff_umma_supports(const Geometry &g)
 
 namespace {
 
-template <int NB, int KT> cudaError_t launch_nb(const DiffArgs &a, int grid, cudaStream_t stream)
+template <int NB, int KT> cudaError_t launch_nb(const DiffArgs &a, int items, cudaStream_t stream)
 {
-    const cudaError_t e = grant_shared_memory<diff_attend_umma_kernel<NB, KT>>();
+    constexpr auto whole = diff_attend_umma_kernel<NB, KT, false>, part = diff_attend_umma_kernel<NB, KT, true>;
+    const bool split = a.splits > 1;
+    cudaError_t e = split ? grant_shared_memory<part>() : grant_shared_memory<whole>();
     if (e != cudaSuccess) return e;
-    return launch_pdl(diff_attend_umma_kernel<NB, KT>, dim3(grid), dim3(kThreads), UmmaTile<NB, KT>::bytes(a.topk), stream, a);
+    e = launch_pdl(split ? part : whole, dim3(items * a.splits), dim3(kThreads), UmmaTile<NB, KT>::bytes(a.topk), stream, a);
+    if (e != cudaSuccess || !split) return e;
+    return launch_pdl(diff_attend_join_kernel<NB>, dim3(items * (a.hd / 8)), dim3(128), 0, stream, a);
+}
+
+constexpr int key_tile(int hd) { return hd <= 64 ? 32 : 64; }
+// Key tiles of a split, at least. One image of one head of 64, whole map: 64 x 64 tokens 68 us in one piece, 34 in splits of
+// 16 tiles (35 of 14); 128 x 128 246 and 224. Below, the second launch costs what the split gains: 4 heads of 128,
+// 32 x 32 tokens 20.3 in one piece, 17.8 in splits of 4, but 8 regions of 64 tokens to a query (56 x 56, 2 heads) 13.1 and 18.4.
+constexpr int kLeastTiles = 16;
+
+// Keys of a split: whole tiles.
+int split_keys(int hd, int topk, int rs, int splits)
+{
+    const int kt = key_tile(hd), tiles = (int)(((long long)topk * rs + kt - 1) / kt);
+    return (tiles + splits - 1) / splits * kt;
 }
 
 }  // namespace
+
+// One round of the GPU: as many CTAs as fit, kLeastTiles key tiles or more to each.
+int diff_umma_splits(const Geometry &g, int num_sms, size_t *scratch)
+{
+    *scratch = 0;
+    const long long items = (long long)g.B * g.R * ((g.rs + 127) / 128) * g.heads;
+    const int kt = key_tile(g.hd), nb = g.hd <= 64 ? 1 : 2;
+    const long long tiles = ((long long)g.topk * g.rs + kt - 1) / kt;
+    long long splits = (long long)num_sms * (nb == 1 ? 2 : 1) / items;
+    if (splits > tiles / kLeastTiles) splits = tiles / kLeastTiles;
+    if (splits < 2) return 1;
+    const int per = split_keys(g.hd, g.topk, g.rs, (int)splits) / kt;
+    splits = (tiles + per - 1) / per;
+    *scratch = (size_t)(items * splits) * 2 * 128 * (16 * nb * sizeof(float4) + sizeof(float2));
+    return (int)splits;
+}
 
 cudaError_t launch_diff_attend_umma(const DiffArgs &args, cudaStream_t stream)
 {
@@ -392,6 +499,8 @@ cudaError_t launch_diff_attend_umma(const DiffArgs &args, cudaStream_t stream)
     const long long items = (long long)a.B * a.R * a.tiles * a.heads;
     if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     a.nitems = (int)items;
+    a.by_splits = FastDiv::of(a.splits);
+    a.per = split_keys(a.hd, a.topk, a.rs, a.splits);
     return a.hd <= 64 ? launch_nb<1, 32>(a, (int)items, stream) : launch_nb<2, 64>(a, (int)items, stream);
 }
 

@@ -213,6 +213,8 @@ bool diff_tile_supports(const Geometry &g);
 cudaError_t launch_diff_attend_tile(const DiffArgs &a, cudaStream_t stream);
 // The tcgen05 ones (bf16, hd a multiple of 16): large regions.
 bool diff_umma_supports(const Geometry &g);
+// The CTAs its keys are split over (1: one CTA meets all keys), and the scratch that takes (0 for 1).
+int diff_umma_splits(const Geometry &g, int num_sms, size_t *scratch);
 cudaError_t launch_diff_attend_umma(const DiffArgs &a, cudaStream_t stream);
 bool diff_backward_umma_supports(const Geometry &g);
 cudaError_t launch_diff_backward_umma(const DiffArgs &a, cudaStream_t stream);

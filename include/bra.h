@@ -207,7 +207,8 @@ bra_status bra_attend_backward(const void *q, const void *k, const void *v, cons
    itself; how a model forms it is the caller's); out shares no memory with q, k or v; other arguments, the
    treatment of idx and the empty row (out = 0) as bra_attend. bf16 runs on the tensor cores (P rounded to
    bf16 for the product with v, everything else fp32), fp32 on CUDA cores; neither depends on
-   bra_set_attend_kernel. BRA_ERR_UNSUPPORTED: hd % 8 != 0, hd > 128 (the limit on a region's row segment,
+   bra_set_attend_kernel. Where few queries meet many keys (bf16), takes at most 24 MB of scratch from the
+   pool. BRA_ERR_UNSUPPORTED: hd % 8 != 0, hd > 128 (the limit on a region's row segment,
    W / n_win * C, holds for routing only). */
 bra_status bra_diff_attend(const void *q, const void *k, const void *v, const int32_t *idx, const float *lambda, void *out,
                            int B, int H, int W, int C, int heads, int n_win, int topk, bra_dtype dtype, void *stream);

@@ -315,3 +315,74 @@ def test_long_map_sampled():
     zero = torch.ones(n, dtype=torch.bool)
     zero[pick] = False
     assert bool((dq.view(-1, hd)[zero.cuda()] == 0).all())
+
+
+# One image, few query tiles and many keys: the keys of a tile are split over several CTAs and joined.
+@pytest.mark.parametrize("shape", [(1, 33, 32, 1, 1, 1, 64), (1, 12, 11, 3, 9, 2, 32), (1, 47, 45, 1, 1, 1, 128), (1, 1, 2500, 1, 1, 1, 48),
+                                   (1, 17, 16, 2, 4, 1, 80), (2, 70, 1, 4, 16, 1, 16)], ids=lambda s: "x".join(map(str, s)))
+def test_split_keys(shape):
+    B, hr, wr, n_win, topk, heads, hd = shape
+    check_all(*make(*shape, BF16, 70), heads, n_win)
+
+
+def test_split_keys_empty_and_infinite():
+    """Splits without keys, rows without keys, splits whose scores are all -inf, rows of nothing else, and a NaN
+    score among them. 9 regions of 132 tokens, 1188 keys in splits of at most 608."""
+    hr, wr, n_win, topk, hd = 12, 11, 3, 9, 64
+    q, k, v, idx, lam, _ = make(1, hr, wr, n_win, topk, 1, hd, BF16, 71)
+    tok = ref.region_tokens(q.shape[1], q.shape[2], n_win)
+    idx[:] = torch.arange(9, dtype=torch.int32, device="cuda")
+    idx[0, 1, 2:] = -1                    # two regions' keys: the first split's
+    idx[0, 2] = 9                         # none
+    idx[0, 3, :7], idx[0, 3, 7:] = 99, 8  # the last region twice
+    idx[0, 4] = 4                         # one region, nine times
+    q[..., 0], k.view(-1, hd)[torch.cat(list(tok[:6])), 0] = 1.0, float("-inf")  # map 1 meets regions 6 to 8 only
+    k.view(-1, hd)[tok[7][5], 40] = float("-inf")
+    q[..., 40] = 0.5
+    q.view(-1, hd)[tok[5][3], 40] = float("nan")
+    out = bra.diff_attend(q, k, v, idx, lam, 1, n_win)
+    assert bra.check_device_error() == 4  # the bad entries
+    Q, K, V, l = (t.double().cpu().reshape(-1, hd) for t in (q, k, v, lam[:, None].expand(1, hd)))
+    got = out.double().cpu().reshape(-1, hd)
+    for r in range(9):
+        named = [int(i) for i in idx[0, r] if 0 <= int(i) < 9]
+        if not named:
+            assert not bool(got[tok[r]].any())
+            continue
+        src = torch.cat([tok[i] for i in named])
+        p1, p2 = (torch.softmax(Q[tok[r]][:, c] @ K[src][:, c].T / 32 ** 0.5, -1) for c in (slice(0, 32), slice(32, 64)))
+        want = (p1 - l[0, 0] * p2) @ V[src]
+        # P and the output are rounded to bf16 (2^-8 relative each); fp32 sums of 1188 terms
+        tol = 2.0 ** -8 * ((p1 + l[0, 0].abs() * p2) @ V[src].abs() + want.abs()) + 1e-4
+        fine = torch.isfinite(want)
+        assert torch.equal(torch.isfinite(got[tok[r]]), fine), r
+        assert bool(((got[tok[r]] - want).abs()[fine] <= tol[fine]).all()), r
+        if r in (1, 4):  # map 1 has nothing but -inf
+            assert not bool(fine.any())
+
+
+def test_split_keys_captured_and_repeated():
+    """The same bits on every run, in graphs with scratch of their own, and beside a whole batch in one piece."""
+    q, k, v, idx, lam, _ = make(1, 40, 40, 1, 1, 1, 64, BF16, 72)
+    first = bra.diff_attend(q, k, v, idx, lam, 1, 1)
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(bra.diff_attend(q, k, v, idx, lam, 1, 1))
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(first, bra.diff_attend(q, k, v, idx, lam, 1, 1))
+    assert all(torch.equal(first, o) for o in outs)
+    # 24 such images leave nothing to split: each element within the roundings of P and of the output, twice
+    many = bra.diff_attend(*(t.expand(24, *t.shape[1:]).contiguous() for t in (q, k, v, idx)), lam, 1, 1)
+    assert torch.equal(many[0], many[23])
+    p = [torch.softmax(q.double().view(-1, 64)[:, c] @ k.double().view(-1, 64)[:, c].T / 32 ** 0.5, -1) for c in (slice(0, 32), slice(32, 64))]
+    weight = (p[0] + lam.double().abs() * p[1]) @ v.double().view(-1, 64).abs()
+    tol = 2 * 2.0 ** -8 * (weight + first.double().view(-1, 64).abs()) + 1e-4
+    assert bool(((many[0] - first[0]).double().abs().view(-1, 64) <= tol).all())
+    assert bra.kernels_per_call("bra_diff_attend", 1, 40, 40, 64, 1, 1, 1, BF16) == 2
+    assert bra.kernels_per_call("bra_diff_attend", 24, 40, 40, 64, 1, 1, 1, BF16) == 1
