@@ -848,15 +848,11 @@ bra_status bra_diff_attend_backward(const void *q, const void *k, const void *v,
     a.err = st->error_word;
     a.stats = reinterpret_cast<float4 *>(ws);
     a.dlam_part = reinterpret_cast<float *>(ws + stats);
-    int32_t *wlist = reinterpret_cast<int32_t *>(ws + stats + parts);
-    int32_t *wstart = reinterpret_cast<int32_t *>(ws + stats + parts + list);
-    a.list = wlist;
-    a.start = wstart;
-    e = bra::launch_diff_invert(a, wlist, wstart, cs);
-    if (e == cudaSuccess)
-        e = kernels == bra::DiffBackward::kUmma  ? bra::launch_diff_backward_umma(a, cs)
-            : kernels == bra::DiffBackward::kMma ? bra::launch_diff_backward_mma(a, cs)
-                                                 : bra::launch_diff_simt(a, true, cs);
+    a.list = reinterpret_cast<int32_t *>(ws + stats + parts);
+    a.start = reinterpret_cast<int32_t *>(ws + stats + parts + list);
+    e = kernels == bra::DiffBackward::kUmma  ? bra::launch_diff_backward_umma(a, cs)
+        : kernels == bra::DiffBackward::kMma ? bra::launch_diff_backward_mma(a, cs)
+                                             : bra::launch_diff_simt(a, true, cs);
     const cudaError_t f = cudaFreeAsync(ws, cs);
     if (e != cudaSuccess) return cuda_fail(e, "differential backward kernels");
     if (f != cudaSuccess) return cuda_fail(f, "cudaFreeAsync(differential backward scratch)");
@@ -1121,7 +1117,7 @@ int bra_kernels_per_call(const char *entry_point, int B, int H, int W, int C, in
                        bra::diff_umma_splits(g, device_state(&st) == BRA_OK ? st->num_sms : 148, &scratch) > 1;
     if (!std::strcmp(entry_point, "bra_diff_attend")) return 1 + split;
     if (!std::strcmp(entry_point, "bra_forward_diff")) return (g.R == 1 ? 1 : route + 1) + split;
-    if (!std::strcmp(entry_point, "bra_diff_attend_backward")) return (long long)g.N * topk > (1LL << 30) ? 0 : 3;
+    if (!std::strcmp(entry_point, "bra_diff_attend_backward")) return (long long)g.N * topk > (1LL << 30) ? 0 : 2;
     return 0;
 }
 

@@ -47,8 +47,8 @@ struct DiffArgs {
     float *dlam;            // [heads]
     float4 *stats;          // [B, heads, N]: L1, L2 (log2 of each map's normaliser), D1, D2
     float *dlam_part;       // [heads, nparts]: sums of D2, one for each (image, region, query tile, warp)
-    const int32_t *list;    // [B, R * topk]: for each region, the regions that route to it, in order
-    const int32_t *start;   // [B, R + 1]: where each region's part of the list starts
+    int32_t *list;          // [B, R * topk]: for each region, the regions that route to it, in order
+    int32_t *start;         // [B, R + 1]: where each region's part of the list starts
     unsigned *err;
     int B, H, W, C, heads, hd, d, n_win, hr, wr, rs, R, topk, N;
     int tiles;      // tiles of a region's tokens
@@ -234,6 +234,69 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
         "r"(a_tmem), "r"(b_low), "r"(idesc), "r"((uint32_t)add), "r"(kDescHigh)
         : "memory");
+}
+
+// A CTA sorts the R * topk routed slots of image b by their region (a stable counting sort): the list of the regions that
+// route to each. Warp w owns the slots [w len, (w + 1) len); count[w][s] counts its slots that name s, then holds where
+// the first of them goes, so that the list keeps the slots' order. The first B CTAs of the backward pass' first
+// launch do this beside the others' queries.
+inline size_t invert_bytes(int warps, int R) { return (size_t)warps * (R + 32) * sizeof(int); }
+template <int WARPS> __device__ __forceinline__ void invert_index(const DiffArgs &a, int b, int *shared)
+{
+    int *total = shared, *count = shared + 32 * WARPS;  // [WARPS][R]
+    const int R = a.R, topk = a.topk;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n = R * topk, len = (n + WARPS - 1) / WARPS;
+    const int begin = min(n, warp * len), end = min(n, begin + len);
+    const int32_t *idx = a.idx + (int64_t)b * n;
+    int32_t *list = a.list + (int64_t)b * n, *start = a.start + (int64_t)b * (R + 1);
+    for (int e = threadIdx.x; e < WARPS * R; e += 32 * WARPS) count[e] = 0;
+    __syncthreads();
+    int *own = count + warp * R;
+    for (int e = begin + lane; e < end; e += 32) {
+        const int s = __ldg(idx + e);
+        if (s >= 0 && s < R) atomicAdd(own + s, 1);
+    }
+    __syncthreads();
+    // exclusive sums over (region, warp), regions in runs of `per` to a thread
+    const int per = (R + 32 * WARPS - 1) / (32 * WARPS);
+    const int s0 = min(R, (int)threadIdx.x * per), s1 = min(R, s0 + per);
+    int sum = 0;
+    for (int s = s0; s < s1; ++s)
+        for (int w = 0; w < WARPS; ++w) sum += count[w * R + s];
+    total[threadIdx.x] = sum;
+    __syncthreads();
+    for (int o = 1; o < 32 * WARPS; o *= 2) {
+        const int add = (int)threadIdx.x >= o ? total[threadIdx.x - o] : 0;
+        __syncthreads();
+        total[threadIdx.x] += add;
+        __syncthreads();
+    }
+    int at = total[threadIdx.x] - sum;
+    for (int s = s0; s < s1; ++s) {
+        start[s] = at;
+        for (int w = 0; w < WARPS; ++w) {
+            const int c = count[w * R + s];
+            count[w * R + s] = at;
+            at += c;
+        }
+    }
+    if (threadIdx.x == 32 * WARPS - 1) start[R] = at;
+    __syncthreads();
+    for (int e0 = begin; e0 < end; e0 += 32) {
+        const int e = e0 + lane;
+        const int s = e < end ? __ldg(idx + e) : -1;
+        const bool ok = s >= 0 && s < R;
+        const unsigned same = __match_any_sync(0xffffffffu, ok ? s : -1);
+        int slot = 0;
+        if (ok) slot = own[s] + __popc(same & ((1u << lane) - 1u));
+        __syncwarp();
+        if (ok) {
+            list[slot] = e / topk;
+            if (lane == 31 - __clz(same)) own[s] = slot + 1;
+        }
+        __syncwarp();
+    }
 }
 
 // x / sum of a row's probabilities, and the row's max + log2(sum) (so that P = 2^(scale S - that)). A row without keys

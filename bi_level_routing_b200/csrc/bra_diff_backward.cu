@@ -2,8 +2,8 @@
 // bra_diff.cuh), heads of 8 to 128 channels in multiples of 8, regions of any size.
 //
 // Nothing is added in memory, so the gradients are the same bits on every run:
-//  invert   lists for each region s the regions that route to it, in the order (region, slot);
-//  queries  one group of warps per 16 WPI query tokens of an (image, region, head): a first pass over
+//  queries  the first B CTAs list for each region s the regions that route to it, in the order (region,
+//           slot); of the others one group of warps per 16 WPI query tokens of an (image, region, head): a first pass over
 //           the routed keys takes both softmaxes' running maximum and sum and, with the same
 //           rescaling, D_i = rowsum(P_i dP); a second forms dS_i and sums dq_i = dS_i k_i in
 //           registers. It leaves L_i = max + log2(sum) and D_i per query, and its sums of D2;
@@ -19,9 +19,11 @@
 // to bf16 once.
 //
 // Few warps and the latency of their gathers bound it: three kernels of 168 registers a thread, 12 warps an SM.
-// 64 images of 28 x 28, 2 heads of 64, 4 regions of 16 tokens to a query: 88 us, of which the queries kernel
-// takes 40, the keys kernel 43 and the lists 4; with 8 regions 182 us.
+// 64 images of 28 x 28, 2 heads of 64, 4 regions of 16 tokens to a query: 83 us, of which the queries kernel
+// takes 40, the keys kernel 43; with 8 regions 178 us. (The lists in a launch of their own: 88.)
 #include "bra_diff.cuh"
+
+#include <algorithm>
 
 namespace bra {
 
@@ -152,75 +154,6 @@ __device__ __forceinline__ void store_rows(const DiffArgs &a, __nv_bfloat16 *bas
 
 }  // namespace
 
-// ------------------------------------------------------------------ who routes to a region
-
-// One CTA of kInvertWarps warps per image: a stable counting sort of the R * topk routed slots by
-// their region. Warp w owns the slots [w len, (w + 1) len); count[w][s] counts its slots that name s,
-// then holds where the first of them goes, so that the list keeps the slots' order.
-constexpr int kInvertWarps = 8;
-
-__global__ void __launch_bounds__(32 * kInvertWarps) diff_invert_kernel(const int32_t *__restrict__ idx, int32_t *list,
-                                                                        int32_t *start, int R, int topk)
-{
-    extern __shared__ int count[];  // [kInvertWarps][R]
-    __shared__ int total[32 * kInvertWarps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n = R * topk, len = (n + kInvertWarps - 1) / kInvertWarps;
-    const int begin = min(n, warp * len), end = min(n, begin + len);
-    const int64_t b = blockIdx.x;
-    idx += b * n;
-    list += b * n;
-    start += b * (R + 1);
-    for (int e = threadIdx.x; e < kInvertWarps * R; e += blockDim.x) count[e] = 0;
-    grid_dependency_wait();
-    __syncthreads();
-    int *own = count + warp * R;
-    for (int e = begin + lane; e < end; e += 32) {
-        const int s = __ldg(idx + e);
-        if (s >= 0 && s < R) atomicAdd(own + s, 1);
-    }
-    __syncthreads();
-    // exclusive sums over (region, warp), regions in runs of `per` to a thread
-    const int per = (R + blockDim.x - 1) / blockDim.x;
-    const int s0 = min(R, (int)threadIdx.x * per), s1 = min(R, s0 + per);
-    int sum = 0;
-    for (int s = s0; s < s1; ++s)
-        for (int w = 0; w < kInvertWarps; ++w) sum += count[w * R + s];
-    total[threadIdx.x] = sum;
-    __syncthreads();
-    for (int o = 1; o < (int)blockDim.x; o *= 2) {
-        const int add = (int)threadIdx.x >= o ? total[threadIdx.x - o] : 0;
-        __syncthreads();
-        total[threadIdx.x] += add;
-        __syncthreads();
-    }
-    int at = total[threadIdx.x] - sum;
-    for (int s = s0; s < s1; ++s) {
-        start[s] = at;
-        for (int w = 0; w < kInvertWarps; ++w) {
-            const int c = count[w * R + s];
-            count[w * R + s] = at;
-            at += c;
-        }
-    }
-    if (threadIdx.x == blockDim.x - 1) start[R] = at;
-    __syncthreads();
-    for (int e0 = begin; e0 < end; e0 += 32) {
-        const int e = e0 + lane;
-        const int s = e < end ? __ldg(idx + e) : -1;
-        const bool ok = s >= 0 && s < R;
-        const unsigned same = __match_any_sync(0xffffffffu, ok ? s : -1);
-        int slot = 0;
-        if (ok) slot = own[s] + __popc(same & ((1u << lane) - 1u));
-        __syncwarp();
-        if (ok) {
-            list[slot] = e / topk;
-            if (lane == 31 - __clz(same)) own[s] = slot + 1;
-        }
-        __syncwarp();
-    }
-}
-
 // ------------------------------------------------------------------ dq, statistics
 
 // SINGLE: all keys fit one tile (topk rs <= KT), whose scores stay in registers between the passes.
@@ -238,7 +171,12 @@ __global__ void __launch_bounds__(32 * kWarps, SINGLE && DK <= 32 ? 3 : 1) diff_
     __nv_bfloat16 *tiles = reinterpret_cast<__nv_bfloat16 *>(mine);  // [stage][K, V][KT][ROW]
     int *count = reinterpret_cast<int *>(mine + (size_t)2 * kStages * KT * ROW * 2);
     int *bases = count + 4;
-    const int item = blockIdx.x * (kWarps / WPI) + group;
+    if (blockIdx.x < a.B) {
+        grid_dependency_wait();
+        invert_index<kWarps>(a, blockIdx.x, reinterpret_cast<int *>(smem4));
+        return;
+    }
+    const int item = (blockIdx.x - a.B) * (kWarps / WPI) + group;
     if (item >= a.nitems) return;  // the whole group: its barriers are its own
     const DiffItem it = diff_item(a, item);
     grid_dependency_wait();
@@ -586,8 +524,9 @@ template <auto Kernel> cudaError_t launch_with(int grid, size_t smem, const Diff
 template <int DK, int WPI, int KT, bool SINGLE> cudaError_t launch_queries(const DiffArgs &a, int grid, cudaStream_t stream)
 {
     constexpr int groups = kWarps / WPI;
-    return launch_with<diff_backward_queries_kernel<DK, WPI, KT, SINGLE>>(
-        grid, groups * ((size_t)(SINGLE ? 2 : 4) * KT * BackTile<DK>::kRow * 2 + round16((size_t)a.topk * 4) + 16), a, stream);
+    const size_t own = groups * ((size_t)(SINGLE ? 2 : 4) * KT * BackTile<DK>::kRow * 2 + round16((size_t)a.topk * 4) + 16);
+    return launch_with<diff_backward_queries_kernel<DK, WPI, KT, SINGLE>>(a.B + grid, std::max(own, invert_bytes(kWarps, a.R)), a,
+                                                                          stream);
 }
 
 // Query tiles of 16 rows: the gradients' accumulators leave no more registers at three CTAs an SM.
@@ -597,7 +536,7 @@ template <int DK, int WPI> cudaError_t launch_one(DiffArgs &a, cudaStream_t stre
     a.tiles = (a.rs + 16 * WPI - 1) / (16 * WPI);
     a.by_tiles = FastDiv::of(a.tiles);
     const long long items = (long long)a.B * a.R * a.tiles * a.heads;
-    if (items * WPI > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (items * WPI + a.B > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     a.nitems = (int)items;
     a.nparts = (int)(items / a.heads * WPI);
     const int grid = (int)((items + groups - 1) / groups);
@@ -655,12 +594,6 @@ void diff_plan(DiffArgs &a, const Geometry &g)
     a.by_heads = FastDiv::of(g.heads);
     a.by_R = FastDiv::of(g.R);
     a.by_topk = FastDiv::of(g.topk);
-}
-
-cudaError_t launch_diff_invert(const DiffArgs &a, int32_t *list, int32_t *start, cudaStream_t stream)
-{
-    const size_t smem = (size_t)kInvertWarps * a.R * sizeof(int);
-    return launch_pdl(diff_invert_kernel, dim3(a.B), dim3(32 * kInvertWarps), smem, stream, a.idx, list, start, a.R, a.topk);
 }
 
 cudaError_t launch_diff_backward_mma(const DiffArgs &args, cudaStream_t stream)

@@ -169,7 +169,12 @@ template <int NB> __global__ void __launch_bounds__(kThreads, 1) diff_backward_q
     int *count = reinterpret_cast<int *>(tmem_slot + 1);
     int *bases = count + 3;
     const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    const DiffItem it = diff_item(a, blockIdx.x);
+    if (blockIdx.x < a.B) {
+        grid_dependency_wait();
+        invert_index<kThreads / 32>(a, blockIdx.x, reinterpret_cast<int *>(smem));
+        return;
+    }
+    const DiffItem it = diff_item(a, blockIdx.x - a.B);
 
     if (threadIdx.x == 0) bar.init(ST, 64);
     if (warp == 8) {
@@ -666,6 +671,8 @@ template <int NB> __global__ void __launch_bounds__(kThreads, 1) diff_backward_k
 // Regions whose 128-row tiles are more than half full. This and the mma.sync kernels, backward: 4 regions of 64
 // tokens to a query (4 heads of 64) 160 against 142 us, of 81 tokens 212 against 309, of 100 tokens 244 against
 // 360; 4 of 100 tokens, heads of 128, 38 against 75.
+static_assert(QueryRing<1>::kOwn + QueryRing<1>::kRing >= (kThreads / 32) * (kMaxRegions + 32) * sizeof(int),
+              "the queries kernel's shared memory holds invert_index's");
 bool diff_backward_umma_supports(const Geometry &g) { return g.hd % 16 == 0 && g.rs > 64; }
 
 namespace {
@@ -681,7 +688,7 @@ template <int NB> cudaError_t launch_nb(const DiffArgs &a, int grid, cudaStream_
     using Q = QueryRing<NB>;
     using K = typename KeyPlan<NB>::Ring;
     const cudaError_t e = launch_with<diff_backward_queries_umma_kernel<NB>>(
-        grid, 1024 + Q::kOwn + Q::kRing + kBarrierBytes + 2 * 6 * 128 * 4 + 16 + 4 * (size_t)a.topk, a, stream);
+        a.B + grid, 1024 + Q::kOwn + Q::kRing + kBarrierBytes + 2 * 6 * 128 * 4 + 16 + 4 * (size_t)a.topk, a, stream);
     if (e != cudaSuccess) return e;
     return launch_with<diff_backward_keys_umma_kernel<NB>>(
         grid > a.heads ? grid : a.heads,
@@ -696,7 +703,7 @@ cudaError_t launch_diff_backward_umma(const DiffArgs &args, cudaStream_t stream)
     a.tiles = (a.rs + 127) / 128;
     a.by_tiles = FastDiv::of(a.tiles);
     const long long items = (long long)a.B * a.R * a.tiles * a.heads;
-    if (items * 4 > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (items * 4 + a.B > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     a.nitems = (int)items;
     a.nparts = (int)(items / a.heads * 4);
     return a.hd <= 64 ? launch_nb<1>(a, (int)items, stream) : launch_nb<2>(a, (int)items, stream);

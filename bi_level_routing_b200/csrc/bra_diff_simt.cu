@@ -13,6 +13,8 @@
 // exchange of tiles and probabilities takes).
 #include "bra_diff.cuh"
 
+#include <algorithm>
+
 namespace bra {
 
 namespace {
@@ -214,7 +216,12 @@ __global__ void __launch_bounds__(32 * WARPS) diff_backward_queries_simt_kernel(
     float *sp = sd + ROWS * stride + warp * 2 * RW * kTileRows;
     int *count = reinterpret_cast<int *>(sd + ROWS * stride + WARPS * 2 * RW * kTileRows);
     int *bases = count + 4;
-    const DiffItem it = diff_item(a, blockIdx.x);
+    if (blockIdx.x < a.B) {
+        grid_dependency_wait();
+        invert_index<WARPS>(a, blockIdx.x, reinterpret_cast<int *>(smem4));
+        return;
+    }
+    const DiffItem it = diff_item(a, blockIdx.x - a.B);
     const int64_t image = (int64_t)it.b * a.N * a.C + it.h * hd;
     const float *gq = static_cast<const float *>(a.q) + image, *gk = static_cast<const float *>(a.k) + image;
     const float *gv = static_cast<const float *>(a.v) + image, *gd = static_cast<const float *>(a.dout) + image;
@@ -480,7 +487,7 @@ template <int WARPS, int RW, int NC> cudaError_t launch_one(DiffArgs &a, bool ba
     a.tiles = (a.rs + L::kRows - 1) / L::kRows;
     a.by_tiles = FastDiv::of(a.tiles);
     const long long items = (long long)a.B * a.R * a.tiles * a.heads;
-    if (items * WARPS > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (items * WARPS + a.B > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     a.nitems = (int)items;
     a.nparts = (int)(items / a.heads * WARPS);
     const size_t tail = 16 + (((size_t)a.topk * 4 + 15) & ~(size_t)15);
@@ -488,8 +495,8 @@ template <int WARPS, int RW, int NC> cudaError_t launch_one(DiffArgs &a, bool ba
     if (!backward)
         return launch_with<diff_attend_simt_kernel<WARPS, RW, NC>>(grid, 32 * WARPS, 4 * L::floats(a.hd, 1, 2) + tail, a,
                            stream);
-    const cudaError_t e = launch_with<diff_backward_queries_simt_kernel<WARPS, RW, NC>>(grid, 32 * WARPS,
-                                      4 * L::floats(a.hd, 2, 2) + tail, a, stream);
+    const cudaError_t e = launch_with<diff_backward_queries_simt_kernel<WARPS, RW, NC>>(
+        a.B + grid, 32 * WARPS, std::max(4 * L::floats(a.hd, 2, 2) + tail, invert_bytes(WARPS, a.R)), a, stream);
     if (e != cudaSuccess) return e;
     return launch_with<diff_backward_keys_simt_kernel<WARPS, RW, NC>>(grid > a.heads ? grid : a.heads, 32 * WARPS,
                        4 * L::floats(a.hd, 2, 3), a, stream);

@@ -180,7 +180,7 @@ def test_kernels_per_call(L):
     stage1 = (64, 56, 56, 64, 1, 7, 1, 1)
     assert L.bra_kernels_per_call(b"bra_diff_attend", *stage1) == 1
     assert L.bra_kernels_per_call(b"bra_forward_diff", *stage1) == 3  # means, affinity and top-k, attention
-    assert L.bra_kernels_per_call(b"bra_diff_attend_backward", *stage1) == 3  # index by region, queries, keys
+    assert L.bra_kernels_per_call(b"bra_diff_attend_backward", *stage1) == 2  # queries, keys
     whole = (1, 64, 4096, 64, 1, 1, 1, 1)  # one region: nothing is routed, and its rows may be of any length
     assert L.bra_kernels_per_call(b"bra_forward_diff", *whole) == 1
     assert L.bra_kernels_per_call(b"bra_forward", *whole) == 0
