@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(32 * kWarps, DK <= 32 ? 4 : 3) diff_attend_til
     if (DENSE) {
         group_barrier<WPI>(group);  // the counts are cleared
         const int32_t *row = a.idx + (int64_t)it.b * a.R * a.topk;
-                constexpr int kAhead = 10;  // index entries in flight for each thread
+        constexpr int kAhead = 10;  // index entries in flight for each thread
         for (int e0 = gtid; e0 < a.R * a.topk; e0 += kAhead * 32 * WPI) {
             int named[kAhead];
 #pragma unroll

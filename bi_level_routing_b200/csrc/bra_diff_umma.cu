@@ -392,50 +392,62 @@ __global__ void __launch_bounds__(kThreads, KT == 32 ? 2 : 1) diff_attend_umma_k
     if (warp == 8) tmem_dealloc(tmem, kCols);
 }
 
-// A CTA joins 8 channels of an item's 128 rows, a row to a thread: each map's splits relative to the largest of their
-// maxima, then out = O1 / l1 - lam O2 / l2.
+// A CTA joins 4 channels of an item's 128 rows, a row to a thread: each map's splits relative to the largest of their
+// maxima, then out = O1 / l1 - lam O2 / l2. Latency bounds it: the loads of kBatch splits of both maps are all in
+// flight at once (one split after the other took 11 us for eight splits of 4096 rows).
 template <int NB> __global__ void __launch_bounds__(128) diff_attend_join_kernel(const DiffArgs a)
 {
-    const int item = blockIdx.x / (a.hd / 8), chunk = blockIdx.x - item * (a.hd / 8);
+    constexpr int kBatch = 8;
+    const int item = blockIdx.x / (a.hd / 4), chunk = blockIdx.x - item * (a.hd / 4);
     const int row = threadIdx.x;
     const DiffItem it = diff_item(a, item);
     grid_dependency_wait();
     const int tok = it.t * 128 + row;
     if (tok >= a.rs) return;
     const float2 *stats = a.split_stats + (int64_t)item * a.splits * 256 + row;
-    const float4 *part = a.split_out + (int64_t)item * a.splits * (2 * 16 * NB * 128) + 2 * chunk * 128 + row;
-    float o[8] = {};
+    const float4 *part = a.split_out + (int64_t)item * a.splits * (2 * 16 * NB * 128) + chunk * 128 + row;
+    const float lam = __ldg(a.lam + it.h);
+    float top[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float4 x[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    bool some = false;
+    for (int s0 = 0; s0 < a.splits; s0 += kBatch) {
+        float2 st[kBatch][2];
+        float4 o[kBatch][2];
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-        float top = -INFINITY, l = 0.f, x[8] = {};
-        bool some = false;
-        for (int s = 0; s < a.splits; ++s) top = fmaxf(top, __ldcg(stats + (2 * s + m) * 128).x);
-#pragma unroll 4
-        for (int s = 0; s < a.splits; ++s) {
-            const float2 st = __ldcg(stats + (2 * s + m) * 128);
-            if (st.y == -1.f) continue;
-            some = true;
-            const float w = st.x == -INFINITY ? 0.f : fast_exp2(st.x - top);
-            l += st.x == -INFINITY ? st.y : st.y * w;
-            const float4 *src = part + (int64_t)(2 * s + m) * (16 * NB * 128);
-            const float4 u = __ldcg(src), v = __ldcg(src + 128);
-            x[0] = fmaf(u.x, w, x[0]);
-            x[1] = fmaf(u.y, w, x[1]);
-            x[2] = fmaf(u.z, w, x[2]);
-            x[3] = fmaf(u.w, w, x[3]);
-            x[4] = fmaf(v.x, w, x[4]);
-            x[5] = fmaf(v.y, w, x[5]);
-            x[6] = fmaf(v.z, w, x[6]);
-            x[7] = fmaf(v.w, w, x[7]);
+        for (int s = 0; s < kBatch; ++s)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const bool in = s0 + s < a.splits;
+                st[s][m] = in ? __ldcg(stats + (2 * (s0 + s) + m) * 128) : make_float2(-INFINITY, -1.f);
+                o[s][m] = in ? __ldcg(part + (int64_t)(2 * (s0 + s) + m) * (16 * NB * 128)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            float most = top[m];
+#pragma unroll
+            for (int s = 0; s < kBatch; ++s) most = fmaxf(most, st[s][m].x);
+            const float corr = top[m] == -INFINITY ? 1.f : fast_exp2(top[m] - most);  // at first there is nothing to scale but 0
+            top[m] = most;
+            l[m] *= corr;
+            x[m] = make_float4(x[m].x * corr, x[m].y * corr, x[m].z * corr, x[m].w * corr);
+#pragma unroll
+            for (int s = 0; s < kBatch; ++s) {
+                if (st[s][m].y == -1.f) continue;
+                some = true;
+                const float w = st[s][m].x == -INFINITY ? 0.f : fast_exp2(st[s][m].x - most);
+                l[m] += st[s][m].x == -INFINITY ? st[s][m].y : st[s][m].y * w;
+                x[m].x = fmaf(o[s][m].x, w, x[m].x);
+                x[m].y = fmaf(o[s][m].y, w, x[m].y);
+                x[m].z = fmaf(o[s][m].z, w, x[m].z);
+                x[m].w = fmaf(o[s][m].w, w, x[m].w);
+            }
         }
-        const float w = over_sum(m ? -__ldg(a.lam + it.h) : 1.f, l, some);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = fmaf(x[i], w, o[i]);
     }
+    const float w1 = over_sum(1.f, l[0], some), w2 = over_sum(-lam, l[1], some);
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + ((int64_t)it.b * a.N + token_at(a, region_at(a, it.r), tok)) * a.C +
-                         it.h * a.hd + 8 * chunk;
-    *reinterpret_cast<uint4 *>(out) =
-        make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+                         it.h * a.hd + 4 * chunk;
+    *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf16x2(fmaf(x[0].x, w1, x[1].x * w2), fmaf(x[0].y, w1, x[1].y * w2)),
+                                                 pack_bf16x2(fmaf(x[0].z, w1, x[1].z * w2), fmaf(x[0].w, w1, x[1].w * w2)));
 }
 
 // Any head the register-tiled kernel takes; regions whose query tiles are more than half full, or just
@@ -457,12 +469,12 @@ template <int NB, int KT> cudaError_t launch_nb(const DiffArgs &a, int items, cu
     if (e != cudaSuccess) return e;
     e = launch_pdl(split ? part : whole, dim3(items * a.splits), dim3(kThreads), UmmaTile<NB, KT>::bytes(a.topk), stream, a);
     if (e != cudaSuccess || !split) return e;
-    return launch_pdl(diff_attend_join_kernel<NB>, dim3(items * (a.hd / 8)), dim3(128), 0, stream, a);
+    return launch_pdl(diff_attend_join_kernel<NB>, dim3(items * (a.hd / 4)), dim3(128), 0, stream, a);
 }
 
 constexpr int key_tile(int hd) { return hd <= 64 ? 32 : 64; }
-// Key tiles of a split, at least. One image of one head of 64, whole map: 64 x 64 tokens 68 us in one piece, 34 in splits of
-// 16 tiles (35 of 14); 128 x 128 246 and 224. Below, the second launch costs what the split gains: 4 heads of 128,
+// Key tiles of a split, at least. One image of one head of 64, whole map: 64 x 64 tokens 68 us in one piece, 28 in splits of
+// 16 tiles (29 of 14); 128 x 128 246 and 225. Below, the second launch costs what the split gains: 4 heads of 128,
 // 32 x 32 tokens 20.3 in one piece, 17.8 in splits of 4, but 8 regions of 64 tokens to a query (56 x 56, 2 heads) 13.1 and 18.4.
 constexpr int kLeastTiles = 16;
 
