@@ -155,13 +155,11 @@ template <int N> __device__ __forceinline__ void cp_async_wait_but()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The new running maximum. While every score so far is -inf it is 0, so that exp2(score - max) is 0,
-// not NaN, and later tiles decide.
-__device__ __forceinline__ float finite_max(float before, float top)
-{
-    const float m = fmaxf(before, top);
-    return m == -INFINITY ? 0.f : m;
-}
+// What scores are taken relative to: the running maximum, or 0 while every score so far is -inf, so that exp2(score - base)
+// is 0, not NaN. The maximum itself stays -inf then: a 0 in its place would be a floor that later, lower scores cannot
+// reach, and below 2^-126 of it they would all count as 0. From a maximum of -inf to any other the sums so far
+// (0, or NaN) are multiplied by exp2(-inf - base) = 0.
+__device__ __forceinline__ float score_base(float max) { return max == -INFINITY ? 0.f : max; }
 
 // A warp goes through ROWS rows, LANES of its lanes to a row: a lane finds the place of one row (locate(row), -1 for none,
 // some dozen instructions), the lanes that copy the row take it from there: copy(row, place).

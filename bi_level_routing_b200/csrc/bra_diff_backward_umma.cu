@@ -320,13 +320,14 @@ template <int NB> __global__ void __launch_bounds__(kThreads, 1) diff_backward_q
                         t1[(x >> 1) & 1] = fmax3(t1[(x >> 1) & 1], __uint_as_float(s1[x]), __uint_as_float(s1[x + 1]));
                         t2[(x >> 1) & 1] = fmax3(t2[(x >> 1) & 1], __uint_as_float(s2[x]), __uint_as_float(s2[x + 1]));
                     }
-                    const float2 m = make_float2(finite_max(mx.x, fmaxf(t1[0], t1[1]) * a.scale_log2),
-                                                 finite_max(mx.y, fmaxf(t2[0], t2[1]) * a.scale_log2));
-                    const float2 corr = make_float2(fast_exp2(mx.x - m.x), fast_exp2(mx.y - m.y));
-                    mx = m;
+                    const float2 most = make_float2(fmaxf(mx.x, fmaxf(t1[0], t1[1]) * a.scale_log2),
+                                                    fmaxf(mx.y, fmaxf(t2[0], t2[1]) * a.scale_log2));
+                    const float2 base = make_float2(score_base(most.x), score_base(most.y));
+                    const float2 corr = make_float2(fast_exp2(mx.x - base.x), fast_exp2(mx.y - base.y));
+                    mx = most;
                     l = __fmul2_rn(l, corr);
                     ed = __fmul2_rn(ed, corr);
-                    const float2 nm = make_float2(-m.x, -m.y);
+                    const float2 nm = make_float2(-base.x, -base.y);
                     float2 la = make_float2(0.f, 0.f), ea = la;
 #pragma unroll
                     for (int x = 0; x < 32; ++x) {
@@ -354,8 +355,8 @@ template <int NB> __global__ void __launch_bounds__(kThreads, 1) diff_backward_q
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             const float *x = part + 128 * m + row, *y = x + 6 * 128;
-            const float top = finite_max(x[0], y[0]);
-            const float wx = fast_exp2(x[0] - top), wy = fast_exp2(y[0] - top);
+            const float top = fmaxf(x[0], y[0]), base = score_base(top);
+            const float wx = fast_exp2(x[0] - base), wy = fast_exp2(y[0] - base);
             const float sum = x[256] * wx + y[256] * wy, num = x[512] * wx + y[512] * wy;
             Ls[m] = log_sum(top, sum, nkeys > 0);
             D[m] = over_sum(num, sum, nkeys > 0);

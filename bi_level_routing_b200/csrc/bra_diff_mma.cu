@@ -163,15 +163,15 @@ __global__ void __launch_bounds__(32 * kWarps) diff_attend_mma_kernel(const Diff
                 float top = -INFINITY;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) top = fmax3(top, s[m][nt][2 * hh], s[m][nt][2 * hh + 1]);
-                const float mn = finite_max(mx[m][hh], quad_max(top) * a.scale_log2);
-                corr[hh] = fast_exp2(mx[m][hh] - mn);
-                mx[m][hh] = mn;
+                const float most = fmaxf(mx[m][hh], quad_max(top) * a.scale_log2), base = score_base(most);
+                corr[hh] = fast_exp2(mx[m][hh] - base);
+                mx[m][hh] = most;
                 float sum = 0.f;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float e = fast_exp2(fmaf(s[m][nt][2 * hh + i], a.scale_log2, -mn));
+                        const float e = fast_exp2(fmaf(s[m][nt][2 * hh + i], a.scale_log2, -base));
                         s[m][nt][2 * hh + i] = e;
                         sum += e;
                     }

@@ -102,8 +102,10 @@ template <int RW, int M> __device__ __forceinline__ void clear(float (&x)[RW][M]
 
 }  // namespace
 
+// Eight warps and the widest heads: 128 registers a thread, so that two CTAs share an SM (4 maps of 17 x 54, 4 heads of 128:
+// 607 us, with the five registers more that the compiler takes by itself, and one CTA, 745); else (0) as the compiler chooses.
 template <int WARPS, int RW, int NC>
-__global__ void __launch_bounds__(32 * WARPS) diff_attend_simt_kernel(const DiffArgs a)
+__global__ void __launch_bounds__(32 * WARPS, WARPS == 8 && NC == 4 ? 2 : 0) diff_attend_simt_kernel(const DiffArgs a)
 {
     constexpr int ROWS = WARPS * RW, THREADS = 32 * WARPS;
     extern __shared__ float4 smem4[];
@@ -169,10 +171,10 @@ __global__ void __launch_bounds__(32 * WARPS) diff_attend_simt_kernel(const Diff
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
                     if (k0 + lane + 32 * x >= nkeys) s[i][x] = -INFINITY;
-                const float mn = finite_max(mx[m][i], warp_max(fmaxf(s[i][0], s[i][1])) * a.scale_log2);
-                const float corr = fast_exp2(mx[m][i] - mn);
-                mx[m][i] = mn;
-                const float e0 = fast_exp2(fmaf(s[i][0], a.scale_log2, -mn)), e1 = fast_exp2(fmaf(s[i][1], a.scale_log2, -mn));
+                const float most = fmaxf(mx[m][i], warp_max(fmaxf(s[i][0], s[i][1])) * a.scale_log2), base = score_base(most);
+                const float corr = fast_exp2(mx[m][i] - base);
+                mx[m][i] = most;
+                const float e0 = fast_exp2(fmaf(s[i][0], a.scale_log2, -base)), e1 = fast_exp2(fmaf(s[i][1], a.scale_log2, -base));
                 l[m][i] = l[m][i] * corr + (e0 + e1);
                 sp[(m * RW + i) * kTileRows + lane] = e0;
                 sp[(m * RW + i) * kTileRows + lane + 32] = e1;
@@ -283,10 +285,10 @@ __global__ void __launch_bounds__(32 * WARPS) diff_backward_queries_simt_kernel(
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
                     if (k0 + lane + 32 * x >= nkeys) s[i][x] = -INFINITY;
-                const float mn = finite_max(mx[m][i], warp_max(fmaxf(s[i][0], s[i][1])) * a.scale_log2);
-                const float corr = fast_exp2(mx[m][i] - mn);
-                mx[m][i] = mn;
-                const float e0 = fast_exp2(fmaf(s[i][0], a.scale_log2, -mn)), e1 = fast_exp2(fmaf(s[i][1], a.scale_log2, -mn));
+                const float most = fmaxf(mx[m][i], warp_max(fmaxf(s[i][0], s[i][1])) * a.scale_log2), base = score_base(most);
+                const float corr = fast_exp2(mx[m][i] - base);
+                mx[m][i] = most;
+                const float e0 = fast_exp2(fmaf(s[i][0], a.scale_log2, -base)), e1 = fast_exp2(fmaf(s[i][1], a.scale_log2, -base));
                 l[m][i] = l[m][i] * corr + (e0 + e1);
                 ed[m][i] = ed[m][i] * corr + fmaf(e0, dp[i][0], e1 * dp[i][1]);
             }

@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(32 * kWarps, DK <= 32 ? 4 : 3) diff_attend_til
             float top = -INFINITY;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) top = fmax3(top, s[m][nt][2 * hh], s[m][nt][2 * hh + 1]);
-            const float mx = finite_max(-INFINITY, quad_max(top) * a.scale_log2);
+            const float base = score_base(quad_max(top) * a.scale_log2);
             float sum = 0.f;
             uint32_t some = 0;
 #pragma unroll
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(32 * kWarps, DK <= 32 ? 4 : 3) diff_attend_til
                 if (DENSE) named = reinterpret_cast<const uint16_t *>(pairs)[(tok0 + g + 8 * hh) * 32 + 4 * nt + t];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float e = fast_exp2(fmaf(s[m][nt][2 * hh + i], a.scale_log2, -mx));
+                    float e = fast_exp2(fmaf(s[m][nt][2 * hh + i], a.scale_log2, -base));
                     if (DENSE) e *= (float)((named >> (8 * i)) & 255u);
                     if (DENSE && m == 0) some |= named;
                     s[m][nt][2 * hh + i] = e;
