@@ -446,8 +446,8 @@ def rope_frequencies(n: int, base: float = 10000.0, scaling: str = "none", facto
       "linear"  every frequency divided by factor (positions interpolated);
       "ntk"     base multiplied by factor^(n / (n - 1)): the fastest stays, the slowest is divided by factor;
       "yarn"    frequencies that turn more than 32 times over trained_extent positions stay, those that turn
-                less than once are divided by factor, a linear ramp (in the number of the pair) between;
-                mscale = 0.1 ln(factor) + 1."""
+                less than once are divided by factor, a linear ramp (in the number of the pair) between, from
+                pair 0 where none turns 32 times; mscale = 0.1 ln(factor) + 1."""
     if n <= 0 or not base > 1.0 or not factor >= 1.0:
         raise ValueError("n must be positive, base above 1 and factor at least 1")
     i = torch.arange(n, dtype=torch.float64)
@@ -462,8 +462,9 @@ def rope_frequencies(n: int, base: float = 10000.0, scaling: str = "none", facto
             raise ValueError("yarn scaling needs trained_extent, the positions seen in training")
         # the (real) pair numbers that turn 32 times and once over the trained extent
         fast, slow = (n * math.log(trained_extent / (turns * 2 * math.pi)) / math.log(base) for turns in (32, 1))
-        low, high = max(math.floor(fast), 0), min(math.ceil(slow), n - 1)
+        low, high = max(math.floor(fast), 0), math.ceil(slow)  # high may lie past the table: then no pair turns less than once
         ramp = ((i - low) / max(high - low, 1e-3)).clamp(0, 1)
+        ramp[i > slow] = 1.0  # also where not even pair 0 turns once
         freqs = freqs * (1 - ramp) + freqs / factor * ramp
         mscale = 0.1 * math.log(factor) + 1.0
     elif scaling not in ("none", "ntk"):
