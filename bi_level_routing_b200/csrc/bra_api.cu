@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 
@@ -695,15 +696,30 @@ static bool overlaps(const void *p, const void *r, size_t bytes)
     return x != y && (x < y ? y - x : x - y) < bytes;
 }
 
-// Whether two buffers of `bytes` share memory at all.
-static bool shares(const void *p, const void *r, size_t bytes) { return p == r || overlaps(p, r, bytes); }
-
-// Whether [p, p + np) and [r, r + nr) share memory.
-static bool meet(const void *p, size_t np, const void *r, size_t nr)
+// Whether a written buffer shares memory with one that is read or with another written one: some CTAs still read what
+// others have written over. Absent (NULL) and empty buffers share nothing.
+struct Buffer {
+    const void *p;
+    size_t bytes;
+};
+static bool meet(const Buffer &a, const Buffer &b)
 {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(r);
-    return x < y ? y - x < np : x - y < nr;
+    if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x < y ? y - x < a.bytes : x - y < b.bytes;
 }
+static bool any_meet(std::initializer_list<Buffer> written, std::initializer_list<Buffer> read)
+{
+    for (const Buffer *w = written.begin(); w != written.end(); ++w) {
+        for (const Buffer &r : read)
+            if (meet(*w, r)) return true;
+        for (const Buffer *other = written.begin(); other != w; ++other)
+            if (meet(*w, *other)) return true;
+    }
+    return false;
+}
+
+static size_t index_bytes(const bra::Geometry &g) { return (size_t)g.B * g.R * g.topk * sizeof(int32_t); }
 
 // The sizes both passes take: heads of a multiple of 8 channels, at most 128.
 static bra_status check_diff(int B, int H, int W, int C, int heads, int n_win, int topk, bra_dtype dtype, bool routes,
@@ -769,7 +785,8 @@ bra_status bra_diff_attend(const void *q, const void *k, const void *v, const in
     if ((s = check_data_ptrs(q, k, v, idx, out)) != BRA_OK) return s;
     if (!lambda || !aligned(lambda, 4)) return BRA_ERR_INVALID_ARG;
     const size_t bytes = (size_t)B * H * W * C * (dtype == BRA_BF16 ? 2 : 4);
-    if (shares(out, q, bytes) || shares(out, k, bytes) || shares(out, v, bytes)) return BRA_ERR_INVALID_ARG;
+    if (any_meet({{out, bytes}}, {{q, bytes}, {k, bytes}, {v, bytes}, {idx, index_bytes(g)}, {lambda, heads * sizeof(float)}}))
+        return BRA_ERR_INVALID_ARG;
     return diff_attend_impl(q, k, v, idx, lambda, out, g, dtype, static_cast<cudaStream_t>(stream));
 }
 
@@ -783,7 +800,8 @@ bra_status bra_forward_diff(const void *q, const void *k, const void *v, int32_t
     if ((s = check_data_ptrs(q, k, v, idx, out)) != BRA_OK) return s;
     if (!lambda || !aligned(lambda, 4)) return BRA_ERR_INVALID_ARG;
     const size_t bytes = (size_t)B * H * W * C * (dtype == BRA_BF16 ? 2 : 4);
-    if (shares(out, q, bytes) || shares(out, k, bytes) || shares(out, v, bytes)) return BRA_ERR_INVALID_ARG;
+    if (any_meet({{out, bytes}, {idx, index_bytes(g)}}, {{q, bytes}, {k, bytes}, {v, bytes}, {lambda, heads * sizeof(float)}}))
+        return BRA_ERR_INVALID_ARG;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (g.R == 1) {  // one region routes to itself whatever its affinity
         const cudaError_t e = cudaMemsetAsync(idx, 0, (size_t)B * sizeof(int32_t), cs);
@@ -812,13 +830,10 @@ bra_status bra_diff_attend_backward(const void *q, const void *k, const void *v,
         !aligned(lambda, 4) || !aligned(dlambda, 4))
         return BRA_ERR_INVALID_ARG;
     const size_t bytes = (size_t)B * H * W * C * (dtype == BRA_BF16 ? 2 : 4);
-    const void *const ins[] = {q, k, v, dout}, *const outs[] = {dq, dk, dv};
-    for (int i = 0; i < 3; ++i) {
-        for (const void *in : ins)
-            if (shares(outs[i], in, bytes)) return BRA_ERR_INVALID_ARG;
-        if (shares(outs[i], outs[(i + 1) % 3], bytes)) return BRA_ERR_INVALID_ARG;
-    }
-    if (shares(dlambda, lambda, (size_t)heads * sizeof(float))) return BRA_ERR_INVALID_ARG;
+    const size_t weights = heads * sizeof(float);
+    if (any_meet({{dq, bytes}, {dk, bytes}, {dv, bytes}, {dlambda, weights}},
+                 {{q, bytes}, {k, bytes}, {v, bytes}, {dout, bytes}, {idx, index_bytes(g)}, {lambda, weights}}))
+        return BRA_ERR_INVALID_ARG;
     // the queries that meet one region are numbered in 31 bits
     if ((long long)g.N * topk > (1LL << 30)) return BRA_ERR_UNSUPPORTED;
     DeviceState *st = nullptr;
@@ -883,6 +898,9 @@ bra_status bra_rope(const void *q, const void *k, void *q_out, void *k_out, cons
     if (overlaps(q, q_out, bytes)) return BRA_ERR_INVALID_ARG;
     if (k && (overlaps(k, k_out, bytes) || q_out == k_out || overlaps(q_out, k_out, bytes) || q_out == k ||
               overlaps(q_out, k, bytes) || k_out == q || overlaps(k_out, q, bytes)))
+        return BRA_ERR_INVALID_ARG;
+    if (any_meet({{q_out, bytes}, {k_out, bytes}},
+                 {{freqs, n * sizeof(float)}, {positions, (size_t)B * H * W * axes * sizeof(int32_t)}}))
         return BRA_ERR_INVALID_ARG;
     DeviceState *st = nullptr;
     const bra_status s = device_state(&st);
@@ -968,7 +986,10 @@ bra_status bra_norm_residual(const void *x, const void *h, const float *gate, in
     // a row is read whole before it is written: an output may be x or h itself, not a part of them
     for (const void *out : {(const void *)s_out, (const void *)y_out})
         if (out && (overlaps(out, x, bytes) || (h && overlaps(out, h, bytes)))) return BRA_ERR_INVALID_ARG;
-    if (s_out && y_out && (s_out == y_out || overlaps(s_out, y_out, bytes))) return BRA_ERR_INVALID_ARG;
+    const size_t row = (size_t)C * sizeof(float);
+    if (any_meet({{s_out, bytes}, {y_out, bytes}},
+                 {{gate, gate_images * row}, {post_weight, row}, {post_bias, row}, {pre_weight, row}, {pre_bias, row}}))
+        return BRA_ERR_INVALID_ARG;
     DeviceState *st = nullptr;
     if ((s = device_state(&st)) != BRA_OK) return s;
     a.s = s_out;
@@ -1007,18 +1028,14 @@ bra_status bra_norm_residual_backward(const void *x, const void *h, const void *
     for (const void *out : {(const void *)dx, (const void *)dh})
         for (const void *in : {x, h, dy, ds})
             if (out && in && overlaps(out, in, bytes)) return BRA_ERR_INVALID_ARG;
-    if (dh && (dx == dh || overlaps(dx, dh, bytes))) return BRA_ERR_INVALID_ARG;
-    // the weights' gradients are written by many CTAs while others still read the weights
     const size_t row = (size_t)C * sizeof(float), rows = gate_images * row;
-    const struct { const void *p; size_t bytes; } read[] = {{gate, rows}, {post_weight, row}, {post_bias, row}, {pre_weight, row},
-                                                            {pre_bias, row}},
-        written[] = {{dgate, rows}, {dpost_weight, row}, {dpost_bias, row}, {dpre_weight, row}, {dpre_bias, row}};
-    for (int i = 0; i < 5; ++i)
-        for (int j = 0; j < 5 && written[i].p; ++j) {
-            if (read[j].p && meet(written[i].p, written[i].bytes, read[j].p, read[j].bytes)) return BRA_ERR_INVALID_ARG;
-            if (j < i && written[j].p && meet(written[i].p, written[i].bytes, written[j].p, written[j].bytes))
-                return BRA_ERR_INVALID_ARG;
-        }
+    const auto weights_meet = [&](std::initializer_list<Buffer> written) {
+        return any_meet(written, {{gate, rows}, {post_weight, row}, {post_bias, row}, {pre_weight, row}, {pre_bias, row}});
+    };
+    if (weights_meet({{dx, bytes}, {dh, bytes}, {dgate, rows}, {dpost_weight, row}, {dpost_bias, row}, {dpre_weight, row}, {dpre_bias, row}}) ||
+        any_meet({{dgate, rows}, {dpost_weight, row}, {dpost_bias, row}, {dpre_weight, row}, {dpre_bias, row}},
+                 {{x, bytes}, {h, bytes}, {dy, bytes}, {ds, bytes}}))
+        return BRA_ERR_INVALID_ARG;
     DeviceState *st = nullptr;
     if ((s = device_state(&st)) != BRA_OK) return s;
     a.dy = dy;

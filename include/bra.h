@@ -204,7 +204,7 @@ bra_status bra_attend_backward(const void *q, const void *k, const void *v, cons
    the tokens of regions idx[b, r, 0..topk-1],
      out = (softmax(s q1 k1^T) - lambda[j] softmax(s q2 k2^T)) v,   s = (hd/2)^-1/2.
    n_win = 1 with topk = 1 attends over the whole map. lambda: device fp32 [heads] (the learned weight
-   itself; how a model forms it is the caller's); out shares no memory with q, k or v; other arguments, the
+   itself; how a model forms it is the caller's); out shares no memory with an input; other arguments, the
    treatment of idx and the empty row (out = 0) as bra_attend. bf16 runs on the tensor cores (P rounded to
    bf16 for the product with v, everything else fp32), fp32 on CUDA cores; neither depends on
    bra_set_attend_kernel. Where few queries meet many keys (bf16), takes at most 24 MB of scratch from the
@@ -214,16 +214,17 @@ bra_status bra_diff_attend(const void *q, const void *k, const void *v, const in
                            int B, int H, int W, int C, int heads, int n_win, int topk, bra_dtype dtype, void *stream);
 
 /* bra_route then bra_diff_attend on one stream (one region routes to itself: idx is cleared and no
-   routing kernel runs). The means are kept in `out` like bra_forward's. */
+   routing kernel runs). The means are kept in `out` like bra_forward's. idx is an output: neither it nor out shares
+   memory with an input or the other. */
 bra_status bra_forward_diff(const void *q, const void *k, const void *v, int32_t *idx, const float *lambda, void *out,
                             int B, int H, int W, int C, int heads, int n_win, int topk, bra_dtype dtype, void *stream);
 
 /* Backward of bra_diff_attend with the routing index held fixed: the gradients of sum(dout * out) by
    q, k, v and lambda. dq, dk, dv: device [B, H, W, C] of dtype, written (regions that nothing routes to
    get 0): each element is summed in fp32 inside one CTA and rounded once, so the gradients are the same
-   bits on every run and nothing wider would be gained; they share no memory with each other or the
-   inputs. dlambda: device fp32 [heads], written (0 for B == 0), not lambda itself. Takes scratch from the pool: 16 bytes for
-   each (token, head), and the index sorted by routed region. BRA_ERR_UNSUPPORTED: as bra_diff_attend, or
+   bits on every run and nothing wider would be gained. dlambda: device fp32 [heads], written (0 for B == 0). The
+   gradients share no memory with each other or an input. Takes scratch from the pool: 16 bytes for each (token,
+   head), and the index sorted by routed region. BRA_ERR_UNSUPPORTED: as bra_diff_attend, or
    H * W * topk > 2^30. */
 bra_status bra_diff_attend_backward(const void *q, const void *k, const void *v, const int32_t *idx, const float *lambda,
                                     const void *dout, void *dq, void *dk, void *dv, float *dlambda, int B, int H, int W,
@@ -252,8 +253,8 @@ typedef enum { BRA_NORM_LAYER = 0, BRA_NORM_RMS = 1 } bra_norm_kind;
    pre_weight NULL: no y (y_out NULL); biases NULL: none; gate NULL: 1. x, h, s_out, y_out: device
    [B, H, W, C] of dtype; weights, biases: device fp32 [C]; gate: device fp32 [gate_images, C] with
    gate_images 1 or B (0 without a gate); all 16-byte aligned. s is rounded for s_out; y is of the s before
-   that rounding. s_out and y_out are distinct and may be x or h themselves. BRA_ERR_UNSUPPORTED:
-   C > 8192. */
+   that rounding. s_out and y_out may each be x or h themselves; otherwise they share no memory with an input
+   (weights, biases and gate included) or each other. BRA_ERR_UNSUPPORTED: C > 8192. */
 bra_status bra_norm_residual(const void *x, const void *h, const float *gate, int gate_images, const float *post_weight,
                              const float *post_bias, const float *pre_weight, const float *pre_bias, float alpha, float eps,
                              bra_norm_kind kind, void *s_out, void *y_out, int B, int H, int W, int C, bra_dtype dtype,
@@ -261,11 +262,10 @@ bra_status bra_norm_residual(const void *x, const void *h, const float *gate, in
 
 /* Backward of bra_norm_residual from its inputs: the gradients of sum(ds * s) + sum(dy * y). dy is given
    exactly where pre_weight is; ds NULL counts as 0 (one of the two is given). dx and, where h is given,
-   dh: device [B, H, W, C] of dtype, written; distinct, and may be one of x, h, dy, ds themselves. The weights'
-   gradients (device fp32, of their weights' shapes; each given exactly where its weight is; they share no
-   memory with each other or a weight) are summed in a fixed order, the same bits on every run; for B == 0
-   they are 0. Takes scratch from the pool: 16 C
-   bytes for each CTA of the launch. */
+   dh: device [B, H, W, C] of dtype, written; each may be one of x, h, dy, ds itself. The weights' gradients
+   (device fp32, of their weights' shapes; each given exactly where its weight is) are summed in a fixed order, the
+   same bits on every run; for B == 0 they are 0. Otherwise the gradients share no memory with an input or each
+   other. Takes scratch from the pool: 16 C bytes for each CTA of the launch. */
 bra_status bra_norm_residual_backward(const void *x, const void *h, const void *dy, const void *ds, const float *gate,
                                       int gate_images, const float *post_weight, const float *post_bias,
                                       const float *pre_weight, const float *pre_bias, float alpha, float eps,
