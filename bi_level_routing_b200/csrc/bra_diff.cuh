@@ -182,11 +182,13 @@ __device__ __forceinline__ void warp_rows(int lane, Locate locate, Copy copy)
 // 2^x of two values on the FMA pipe, for probabilities that are rounded to bf16: x = n + f with n the
 // nearest integer (added to 1.5 2^23, where a float's last bit counts ones), 2^f a cubic fitted to least
 // relative error on [-1/2, 1/2] (7.5e-5, a 26th of a bf16 rounding), n added to its exponent. x below
-// -126 counts as -126. A NaN or +inf x gives some finite value: the caller looks for them in the row's maximum.
+// -126.998 counts as that: 1.0013 2^-127 loses its leading one with the exponent, and what is left rounds to 0 in bf16, so
+// that a masked key's value counts 0 times. A NaN or +inf x gives some finite value: the caller looks for them in the
+// row's maximum.
 __device__ __forceinline__ float2 poly_exp2(float2 x)
 {
     const float2 magic = make_float2(12582912.f, 12582912.f), back = make_float2(-12582912.f, -12582912.f);
-    x = make_float2(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f));
+    x = make_float2(fmaxf(x.x, -126.998f), fmaxf(x.y, -126.998f));
     const float2 n = __fadd2_rn(x, magic);
     const float2 m = __fadd2_rn(n, back);
     const float2 f = __ffma2_rn(m, make_float2(-1.f, -1.f), x);

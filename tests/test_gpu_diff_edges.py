@@ -108,3 +108,21 @@ def test_scores_below_a_masked_tile(shape, low, dead_first):
     for name, t in got.items():
         ref.check(t, want[name], want[name + "_tol"], name)
     assert bra.check_device_error() == 0
+
+
+@pytest.mark.parametrize("dead_first", [True, False], ids=["masked_first", "masked_last"])
+@pytest.mark.parametrize("shape", MASKED, ids=lambda s: "x".join(map(str, s)).replace("torch.", ""))
+def test_values_of_masked_keys(shape, dead_first):
+    """A key with a score of -inf has a probability of exactly 0: its value counts 0 times, the type's largest as well; an
+    infinite one is 0 times infinity, NaN, in its own channel."""
+    hr, wr, n_win, hd, dtype = shape
+    q, k, v, idx, lam, dout, dead = masked_inputs(hr, wr, n_win, hd, dtype, dead_first, float("-inf"), 0.0, 6)
+    v.view(-1, hd)[dead.cuda()] = torch.finfo(dtype).max
+    want = masked_reference(q, k, v, lam, dout, n_win, dead)
+    out = bra.diff_attend(q, k, v, idx, lam, 1, n_win)
+    ref.check(out, want["out"], want["out_tol"], "out")
+    v.view(-1, hd)[dead.cuda(), 5] = float("inf")
+    out = bra.diff_attend(q, k, v, idx, lam, 1, n_win)
+    assert bool(torch.isnan(out[..., 5]).all())
+    rest = torch.arange(hd) != 5
+    ref.check(out[..., rest.cuda()], want["out"][..., rest], want["out_tol"][..., rest], "out beside the infinity")
