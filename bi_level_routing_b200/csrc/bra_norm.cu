@@ -29,10 +29,13 @@ namespace bra {
 
 namespace {
 
-// CTAs an SM in the forward pass: of 256 threads, and of 512
-// (200704 rows of 64 channels: two CTAs of 256 21.3 us, three 20.0, four 20.9)
-constexpr int kForwardCtas = 3, kForwardWide = 1;
 constexpr int block_threads(int tpr) { return tpr > 256 ? tpr : 256; }
+// CTAs an SM: the kernels' launch bounds, what the grid is planned for, and what their shared memory must let in. Of 256
+// threads three in the forward pass (200704 rows of 64 channels: two 21.3 us, three 20.0, four 20.9), two where a
+// thread has more than 8 elements, whose channel arrays are in shared memory (8192 rows of 4096, RMS: 45 us; three, with
+// one array there and the others from L1, 54), and in the backward pass; of 512 one.
+constexpr int sm_ctas(int threads, int elements, bool backward) { return threads > 256 ? 1 : backward || elements > 8 ? 2 : 3; }
+constexpr bool sm_holds(int ctas, size_t smem) { return ctas * (smem + 1024) <= 228 * 1024; }  // 1 KB a CTA is the system's
 
 // Row groups in the rings. Forward, 200704 rows of 64 channels: 2 23.8 us, 3 20.0, 4 20.0. Backward, 50176 rows of 128
 // channels: 2 32.8 us, 3 29.2, 4 30.1; rows of two vectors a thread hold two CTAs on an SM only with 2 (8192
@@ -309,10 +312,11 @@ __device__ __forceinline__ void store_row(void *base, int64_t row, const NormArg
 }  // namespace
 
 template <typename T, int TPR, int VPT>
-__global__ void __launch_bounds__(block_threads(TPR), TPR > 256 ? kForwardWide : kForwardCtas) norm_residual_kernel(const NormArgs a)
+__global__ void __launch_bounds__(block_threads(TPR), sm_ctas(block_threads(TPR), Vec16<T>::N * VPT, false)) norm_residual_kernel(const NormArgs a)
 {
     constexpr int V = Vec16<T>::N, E = V * VPT, RPC = block_threads(TPR) / TPR;
-    constexpr bool kKeep = E <= 8;  // the channel arrays stay in registers (4 E of them); else they come from L1
+    // the channel arrays stay in registers (4 E of them); else the factors come from shared memory, the biases from L1
+    constexpr bool kKeep = E <= 8;
     extern __shared__ float4 smem4[];
     using Ring = RowRing<T, TPR, VPT, 2, kForwardStages>;
     float *red = reinterpret_cast<float *>(smem4) + Ring::kBytes / 4;
@@ -366,7 +370,7 @@ __global__ void __launch_bounds__(block_threads(TPR), TPR > 256 ? kForwardWide :
 #pragma unroll
                 for (int i = 0; i < E; ++i) s[i] += fmaf(p[i], w[0][i], w[1][i]);
             } else {
-                load_branch<TPR, V, VPT>(w[0], gate, a.post_w, 1.f, a.nvec, lane);
+                stash.read(0, w[0]);
 #pragma unroll
                 for (int i = 0; i < E; ++i) s[i] = fmaf(p[i], w[0][i], s[i]);
                 if (a.post_b) {
@@ -400,7 +404,7 @@ __global__ void __launch_bounds__(block_threads(TPR), TPR > 256 ? kForwardWide :
 
 // part [units][4][C]: each CTA's column sums A, sum dy s^, S, sum dy (the last two where BIAS)
 template <typename T, int TPR, int VPT, bool BIAS>
-__global__ void __launch_bounds__(block_threads(TPR), TPR > 256 ? 1 : 2) norm_residual_backward_kernel(const NormArgs a)
+__global__ void __launch_bounds__(block_threads(TPR), sm_ctas(block_threads(TPR), Vec16<T>::N * VPT, true)) norm_residual_backward_kernel(const NormArgs a)
 {
     constexpr int V = Vec16<T>::N, E = V * VPT, RPC = block_threads(TPR) / TPR, THREADS = block_threads(TPR);
     constexpr int SUMS = BIAS ? 4 : 2;
@@ -636,14 +640,15 @@ template <typename T, int TPR, int VPT> cudaError_t launch_norm(const NormArgs &
 {
     constexpr int threads = block_threads(TPR);
     constexpr int E = Vec16<T>::N * VPT;
-    constexpr size_t red = 128 * sizeof(float) + (E > 8 || (VPT > 1) ? Stash<TPR, E>::kBytes : 0);
-    if (!backward)
-        return launch_with<norm_residual_kernel<T, TPR, VPT>>(
-            threads, RowRing<T, TPR, VPT, 2, kForwardStages>::kBytes + red, a, stream);
+    constexpr size_t red = 128 * sizeof(float);
+    constexpr size_t forward = RowRing<T, TPR, VPT, 2, kForwardStages>::kBytes + red + (E > 8 ? Stash<TPR, E>::kBytes : 0);
+    static_assert(sm_holds(sm_ctas(threads, E, false), forward), "the planned CTAs fit an SM");
+    if (!backward) return launch_with<norm_residual_kernel<T, TPR, VPT>>(threads, forward, a, stream);
     // the ring, later the row groups' column sums
     constexpr size_t ring = RowRing<T, TPR, VPT, 4, kBackwardStages<VPT>>::kBytes;
     constexpr size_t sums = threads > TPR ? sizeof(float) * Vec16<T>::N * VPT * threads : 0;
-    constexpr size_t smem = (ring > sums ? ring : sums) + red;
+    constexpr size_t smem = (ring > sums ? ring : sums) + red + (VPT > 1 ? Stash<TPR, E>::kBytes : 0);
+    static_assert(sm_holds(sm_ctas(threads, E, true), smem), "the planned CTAs fit an SM");
     cudaError_t e = a.post_b || a.pre_b
                         ? launch_with<norm_residual_backward_kernel<T, TPR, VPT, true>>(threads, smem, a, stream)
                         : launch_with<norm_residual_backward_kernel<T, TPR, VPT, false>>(threads, smem, a, stream);
@@ -675,8 +680,7 @@ void norm_plan(NormArgs &a, bool backward, int num_sms)
     int tpr, vpt;
     row_shape(a.nvec, tpr, vpt);
     const int threads = block_threads(tpr);
-    // CTAs that an SM holds: the kernels' launch bounds
-    split_rows(a, threads, tpr, num_sms * (threads > 256 ? (backward ? 1 : kForwardWide) : backward ? 2 : kForwardCtas));
+    split_rows(a, threads, tpr, num_sms * sm_ctas(threads, a.C / a.nvec * vpt, backward));
 }
 
 cudaError_t launch_norm_residual(const NormArgs &a, bool bf16, bool backward, cudaStream_t stream)
