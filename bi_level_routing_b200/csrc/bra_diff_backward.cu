@@ -18,9 +18,13 @@
 // of which dq keeps only what differs between keys: for dq, dS is two bf16 terms. Each gradient is rounded
 // to bf16 once.
 //
-// Few warps and the latency of their gathers bound it: three kernels of 168 registers a thread, 12 warps an SM.
-// 64 images of 28 x 28, 2 heads of 64, 4 regions of 16 tokens to a query: 83 us, of which the queries kernel
-// takes 40, the keys kernel 43; with 8 regions 178 us. (The lists in a launch of their own: 88.)
+// Few warps and the latency of their gathers bound it: two kernels of 168 registers a thread, three CTAs (12 warps) an
+// SM, for heads of up to 64 channels; above, 242 to 255 registers and two CTAs (8 warps). 64 images of 28 x 28, 2 heads of
+// 64, 4 regions of 16 tokens to a query: 83 us, of which the queries kernel takes 40, the keys kernel 43; with 8
+// regions 175 us. (The lists in a launch of their own: 88.) Regions of less than 16 tokens leave rows of a warp's tile
+// empty: 64 images of 14 x 14, 4 heads of 64, 16 regions of 4 tokens 141 us; of 7 x 7, 8 heads, all 49 one-token regions
+// 251 us. One CTA sorts an image's index, and where regions are small and many are routed the queries' launch waits
+// for it: one image of 256 one-token regions, all routed, 2 heads, 341 us; of 1024, 5.1 ms, of which the sort takes 4.9.
 #include "bra_diff.cuh"
 
 #include <algorithm>
@@ -165,7 +169,7 @@ __global__ void __launch_bounds__(32 * kWarps, SINGLE && DK <= 32 ? 3 : 1) diff_
     constexpr int HP = L::kHp, ROW = L::kRow, NK = L::kNk, NT = KT / 8;
     extern __shared__ float4 smem4[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int group = warp / WPI, wg = warp % WPI, gtid = threadIdx.x % (32 * WPI);
+    const int group = warp / WPI, wg = warp % WPI;
     const size_t group_bytes = (size_t)2 * kStages * KT * ROW * 2 + (((size_t)a.topk * 4 + 15) & ~(size_t)15) + 16;
     uint8_t *mine = reinterpret_cast<uint8_t *>(smem4) + group * group_bytes;
     __nv_bfloat16 *tiles = reinterpret_cast<__nv_bfloat16 *>(mine);  // [stage][K, V][KT][ROW]

@@ -12,11 +12,11 @@
 //   rows), so that P1 - lam P2 and dS_i again multiply from where they were scored: dv += (P1 - lam P2)^T dout,
 //   dk_i += dS_i^T q_i.
 //
-// 10 hd multiply-adds a query-key pair are due; recomputing the scores and the second term of dS make them 18, and
-// six exponentials. 4096-token maps (4 images, 4 heads of 128) take 1050 us: 570 the queries kernel, where the
-// exponentials (16 a cycle and SM) and the score products share the time, 430 the keys kernel, whose
-// products of 32 columns are bound by reading their 128-row operands from shared memory. 512 CTAs of one an
-// SM are 3.46 rounds of 148. Precision as in bra_diff_backward.cu.
+// Five products of hd channels, 10 hd operations a query-key pair, and two exponentials are due. Scoring three times and
+// the second term of dS make them 20 hd and six. 4096-token maps (4 images, 4 heads of 128) take 1020 us, some 590 the
+// queries kernel, where the exponentials (16 a cycle and SM) and the score products share the time, 430 the keys
+// kernel, whose products of 32 columns are bound by reading their 128-row operands from shared memory. 512 CTAs
+// of one an SM are 3.46 rounds of 148. Precision as in bra_diff_backward.cu.
 #include "bra_diff.cuh"
 
 namespace bra {

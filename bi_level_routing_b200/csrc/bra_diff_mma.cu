@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(32 * kWarps) diff_attend_mma_kernel(const Diff
     constexpr int HP = L::kHp, ROW = L::kRow, NK = DK / 16, NT = KT / 8;
     extern __shared__ float4 smem4[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int group = warp / WPI, wg = warp % WPI, gtid = threadIdx.x % (32 * WPI);
+    const int group = warp / WPI, wg = warp % WPI;
     uint8_t *mine = reinterpret_cast<uint8_t *>(smem4) + (size_t)group * L::group_bytes(a.topk);
     __nv_bfloat16 *tiles = reinterpret_cast<__nv_bfloat16 *>(mine);  // [stage][K, V][KT][ROW]
     int *count = reinterpret_cast<int *>(mine + (size_t)4 * KT * ROW * 2);

@@ -1,6 +1,6 @@
 // bra_diff_simt.cu -- differential attention and its gradients of fp32 maps on CUDA cores (formula in bra_diff.cuh), hd a
-// multiple of 8 up to 128, regions of any size. The FMA pipe bounds it: 6 hd operations a query-key pair forward, 18 hd
-// backward (both passes score again).
+// multiple of 8 up to 128, regions of any size: 6 hd operations a query-key pair forward (4 hd are due; the two maps'
+// sums run apart), 18 hd backward (10 hd are due; both passes score again, one of them twice).
 //
 // A CTA owns WARPS x RW token rows of one (image, region, head), RW of them a warp's; the tokens they
 // meet (keys for the forward pass and dq, queries for dk and dv) come through shared memory in tiles of
@@ -9,8 +9,10 @@
 // FMA pipe is the bound from RW = 8 on). The products with the tile's channels turn round: lanes
 // over channels, the probabilities of four tile rows read as one broadcast.
 // As in bra_diff_backward.cu, nothing is added in memory. Forward, 4 images of 45 x 35, 2 heads of 48, 3 regions
-// of 63 tokens to a query: 50 us from cold, a third of the FMA rate (12 warps an SM hide too little of what the
-// exchange of tiles and probabilities takes).
+// of 63 tokens to a query: 46 us, a third of the FMA rate. Many keys take warps of four rows, for which both products are
+// bound by shared memory (12 wavefronts for 8 cycles of FMA, 8 for 4), and heads of 128 one CTA of eight warps an SM in
+// the backward pass: 4 whole maps of 17 x 54, 4 heads of 128, 610 us forward and 2050 us backward, 15
+// and 11 % of that rate by the operations due.
 #include "bra_diff.cuh"
 
 #include <algorithm>

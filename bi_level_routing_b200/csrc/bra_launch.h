@@ -220,7 +220,6 @@ bool diff_backward_umma_supports(const Geometry &g);
 cudaError_t launch_diff_backward_umma(const DiffArgs &a, cudaStream_t stream);
 cudaError_t launch_diff_backward_mma(const DiffArgs &a, cudaStream_t stream);
 cudaError_t launch_diff_simt(const DiffArgs &a, bool backward, cudaStream_t stream);
-// list [B, R * topk] and start [B, R + 1]: for each region the regions that route to it, in order.
 // Partial sums that a family of backward kernels leaves for each head's dlam.
 enum class DiffBackward { kSimt, kMma, kUmma };
 long long diff_backward_parts(const Geometry &g, DiffBackward kernels);
